@@ -273,6 +273,30 @@ int gemm_run_ws(const gemm_plan *plan, const void *A, const void *B, void *C,
                 hipStream_t stream);
 
 /*
+ * gemm_run_res -- the fused epilogue with a residual and a saved
+ * pre-activation, for layers whose output joins a residual stream and for
+ * training:
+ *
+ *   z[m][n] = (acc[m][n] * sa(m)) * sb(n)  (+ bias[n])      as gemm_run_ex
+ *   C[m][n] = cvt( act(z[m][n]) + residual[m][n] )          one rounding
+ *   preact[m][n] = cvt( z[m][n] )
+ *
+ *   A, B, C, epi, stream  as for gemm_run_ex (MX plans: gemm_run_mx_res).
+ *   residual  device pointer, M x N of C's type, 16-byte aligned, or NULL (0).
+ *             It may be C itself (C is then updated in place); otherwise it
+ *             must not overlap C.
+ *   preact    device pointer, M x N of C's type, 16-byte aligned, or NULL.
+ *             Must not overlap A, B, C, the residual or the workspace.
+ *   workspace, workspace_bytes  as for gemm_run_ws (NULL, 0: no split).  It
+ *             must not overlap the residual either.
+ * Plans with GEMM_KERNEL_AUTO or GEMM_KERNEL_TILE256; the other explicit
+ * kernel choices give GEMM_ERR_UNSUPPORTED when a residual or preact is
+ * given.  With neither, the call is gemm_run_ws.  Errors as gemm_run_ws.
+ */
+int gemm_run_res(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
+                 const void *residual, void *preact, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * gemm_run_ws_noalloc -- gemm_run_ws on the library's own static workspace,
  * for callers that cannot allocate device memory (code under HIP graph
  * capture, tight serving loops, harnesses that forbid allocation).  The
@@ -347,6 +371,14 @@ int gemm_preshuffle_bscale(const gemm_plan *plan, int operand, const void *scale
  */
 int gemm_run_mx(const gemm_plan *plan, const void *A, const void *A_bscale, const void *B,
                 const void *B_bscale, void *C, const gemm_epilogue_args *epi, hipStream_t stream);
+
+/*
+ * gemm_run_mx_res -- gemm_run_mx with the residual and pre-activation of
+ * gemm_run_res (no split K).
+ */
+int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, const void *B,
+                    const void *B_bscale, void *C, const gemm_epilogue_args *epi, const void *residual,
+                    void *preact, hipStream_t stream);
 
 /*
  * Integer operands (GEMM_I8_OUT_BF16, GEMM_W4A8_OUT_BF16).  The pages' int8

@@ -713,6 +713,7 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
     if (!plan)
         return fail(GEMM_ERR_INVALID_ARG, "NULL plan");
     const gemm_plan_info &I = plan->info;
+    const bool ex = epi.res || epi.pre;
     if (I.M == 0 || I.N == 0) {
         ok();
         return GEMM_OK;
@@ -746,7 +747,7 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         a.sa_img = (const uint8_t *)sa_img;
         a.sb_img = (const uint8_t *)sb_img;
         a.s_groups = (int32_t)scale_groups(I.K);
-        e = plan->skinny->launch(a, I.grid, stream);
+        e = (ex ? plan->skinny->launch_ex : plan->skinny->launch)(a, I.grid, stream);
     } else {
         tg::TiledArgs a{};
         a.A = A;
@@ -769,7 +770,7 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         a.sa_img = (const uint8_t *)sa_img;
         a.sb_img = (const uint8_t *)sb_img;
         a.s_groups = (int32_t)scale_groups(I.K);
-        e = plan->tiled->launch(a, stream);
+        e = (ex ? plan->tiled->launch_ex : plan->tiled->launch)(a, stream);
     }
     if (e != hipSuccess)
         return fail(GEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
@@ -824,11 +825,34 @@ int run_split(const gemm_plan *plan, const void *A, const void *B, void *C, void
     r.N = (int32_t)I.N;
     r.splits = plan->splits;
     r.out = out_of(I.dtype);
+    r.ex = epi.res || epi.pre;
     e = tg::launch_split_reduce(r, stream);
     if (e != hipSuccess)
         return fail(GEMM_ERR_HIP, "split-K reduction launch: %s", hipGetErrorString(e));
     ok();
     return GEMM_OK;
+}
+
+// Split K through a caller's workspace of at least workspace_bytes(plan).
+int run_ws_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const tg::EpiArgs &e, void *workspace,
+                hipStream_t stream)
+{
+    const size_t need = workspace_bytes(plan);
+    const gemm_plan_info &I = plan->info;
+    if (!A || !B || !C)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL A, B or C");
+    if (misaligned(A) || misaligned(B) || misaligned(C) || misaligned(workspace))
+        return fail(GEMM_ERR_INVALID_ARG, "A, B, C and the workspace must be 16-byte aligned");
+    const size_t cbytes = (size_t)I.M * I.N * I.out_bytes;
+    const size_t abytes = (size_t)I.M * plan->kbytes, bbytes = (size_t)I.N * plan->kbytes_b;
+    if (overlap(C, cbytes, A, abytes) || overlap(C, cbytes, B, bbytes))
+        return fail(GEMM_ERR_INVALID_ARG, "C overlaps A or B");
+    if (overlap(workspace, need, A, abytes) || overlap(workspace, need, B, bbytes) ||
+        overlap(workspace, need, C, cbytes))
+        return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps A, B or C");
+    if (int rc = check_device())
+        return rc;
+    return run_split(plan, A, B, C, workspace, e, stream);
 }
 
 // The epilogue description -> kernel arguments (GEMM_OK or an error).
@@ -859,6 +883,47 @@ int epi_from(const gemm_epilogue_args *epi, tg::EpiArgs *e)
     e->sb_cols = epi->scale_b_per_col;
     static const int kAct[] = {tg::kActNone, tg::kActNone, tg::kActRelu, tg::kActSilu, tg::kActGelu};
     e->act = kAct[epi->epilogue];
+    return GEMM_OK;
+}
+
+// Residual and pre-activation of gemm_run_res / gemm_run_mx_res -> kernel
+// arguments (the epilogue `e` has been filled by epi_from).
+int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C, const void *residual, void *preact,
+             tg::EpiArgs *e)
+{
+    if (!plan)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL plan");
+    const gemm_plan_info &I = plan->info;
+    const size_t cbytes = (size_t)I.M * I.N * I.out_bytes;
+    if ((residual && misaligned(residual)) || (preact && misaligned(preact)))
+        return fail(GEMM_ERR_INVALID_ARG, "residual and preact must be 16-byte aligned");
+    if (residual && residual != C && overlap(residual, cbytes, C, cbytes))
+        return fail(GEMM_ERR_INVALID_ARG, "residual must be C itself or not overlap it");
+    if (preact && (overlap(preact, cbytes, C, cbytes) || overlap(preact, cbytes, residual, residual ? cbytes : 0) ||
+                   overlap(preact, cbytes, A, (size_t)I.M * plan->kbytes) ||
+                   overlap(preact, cbytes, B, (size_t)I.N * plan->kbytes_b)))
+        return fail(GEMM_ERR_INVALID_ARG, "preact overlaps A, B, C or the residual");
+    if ((residual || preact) &&
+        (I.kernel == 1 ? plan->skinny->launch_ex == nullptr : plan->tiled->launch_ex == nullptr))
+        return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no residual epilogue (GEMM_KERNEL_AUTO and "
+                                          "GEMM_KERNEL_TILE256 have)");
+    e->res = residual;
+    e->pre = preact;
+    return GEMM_OK;
+}
+
+int check_mx(const gemm_plan *plan, const void *A_bscale, const void *B_bscale)
+{
+    if (!plan)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL plan");
+    if (!is_mx(plan->info.dtype))
+        return fail(GEMM_ERR_INVALID_ARG, "gemm_run_mx needs an MX plan");
+    if (plan->info.M && plan->info.N && plan->info.K) {
+        if (!A_bscale || !B_bscale)
+            return fail(GEMM_ERR_INVALID_ARG, "NULL block-scale image");
+        if (!aligned(A_bscale, 16) || !aligned(B_bscale, 16))
+            return fail(GEMM_ERR_INVALID_ARG, "block-scale images must be 16-byte aligned");
+    }
     return GEMM_OK;
 }
 
@@ -911,21 +976,28 @@ int gemm_run_ws(const gemm_plan *plan, const void *A, const void *B, void *C, co
     const size_t need = workspace_bytes(plan);
     if (need == 0 || !workspace || workspace_bytes_given < need)
         return run_impl(plan, A, B, C, e, stream);
-    const gemm_plan_info &I = plan->info;
-    if (!A || !B || !C)
-        return fail(GEMM_ERR_INVALID_ARG, "NULL A, B or C");
-    if (misaligned(A) || misaligned(B) || misaligned(C) || misaligned(workspace))
-        return fail(GEMM_ERR_INVALID_ARG, "A, B, C and the workspace must be 16-byte aligned");
-    const size_t cbytes = (size_t)I.M * I.N * I.out_bytes;
-    const size_t abytes = (size_t)I.M * plan->kbytes, bbytes = (size_t)I.N * plan->kbytes_b;
-    if (overlap(C, cbytes, A, abytes) || overlap(C, cbytes, B, bbytes))
-        return fail(GEMM_ERR_INVALID_ARG, "C overlaps A or B");
-    if (overlap(workspace, need, A, abytes) || overlap(workspace, need, B, bbytes) ||
-        overlap(workspace, need, C, cbytes))
-        return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps A, B or C");
-    if (int rc = check_device())
+    return run_ws_impl(plan, A, B, C, e, workspace, stream);
+}
+
+int gemm_run_res(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
+                 const void *residual, void *preact, void *workspace, size_t workspace_bytes_given,
+                 hipStream_t stream)
+{
+    if (int rc = reject_mx(plan))
         return rc;
-    return run_split(plan, A, B, C, workspace, e, stream);
+    tg::EpiArgs e;
+    if (int rc = epi_from(epi, &e))
+        return rc;
+    if (int rc = ext_from(plan, A, B, C, residual, preact, &e))
+        return rc;
+    const size_t need = workspace_bytes(plan);
+    if (need == 0 || !workspace || workspace_bytes_given < need)
+        return run_impl(plan, A, B, C, e, stream);
+    const size_t cbytes = (size_t)plan->info.M * plan->info.N * plan->info.out_bytes;
+    if (overlap(workspace, need, residual, residual ? cbytes : 0) ||
+        overlap(workspace, need, preact, preact ? cbytes : 0))
+        return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps the residual or preact");
+    return run_ws_impl(plan, A, B, C, e, workspace, stream);
 }
 
 int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, void *C,
@@ -1011,18 +1083,23 @@ int gemm_preshuffle_bscale(const gemm_plan *plan, int operand, const void *scale
 int gemm_run_mx(const gemm_plan *plan, const void *A, const void *A_bscale, const void *B, const void *B_bscale,
                 void *C, const gemm_epilogue_args *epi, hipStream_t stream)
 {
-    if (!plan)
-        return fail(GEMM_ERR_INVALID_ARG, "NULL plan");
-    if (!is_mx(plan->info.dtype))
-        return fail(GEMM_ERR_INVALID_ARG, "gemm_run_mx needs an MX plan");
-    if (plan->info.M && plan->info.N && plan->info.K) {
-        if (!A_bscale || !B_bscale)
-            return fail(GEMM_ERR_INVALID_ARG, "NULL block-scale image");
-        if (!aligned(A_bscale, 16) || !aligned(B_bscale, 16))
-            return fail(GEMM_ERR_INVALID_ARG, "block-scale images must be 16-byte aligned");
-    }
+    if (int rc = check_mx(plan, A_bscale, B_bscale))
+        return rc;
     tg::EpiArgs e;
     if (int rc = epi_from(epi, &e))
+        return rc;
+    return run_impl(plan, A, B, C, e, stream, A_bscale, B_bscale);
+}
+
+int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, const void *B, const void *B_bscale,
+                    void *C, const gemm_epilogue_args *epi, const void *residual, void *preact, hipStream_t stream)
+{
+    if (int rc = check_mx(plan, A_bscale, B_bscale))
+        return rc;
+    tg::EpiArgs e;
+    if (int rc = epi_from(epi, &e))
+        return rc;
+    if (int rc = ext_from(plan, A, B, C, residual, preact, &e))
         return rc;
     return run_impl(plan, A, B, C, e, stream, A_bscale, B_bscale);
 }

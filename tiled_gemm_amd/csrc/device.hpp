@@ -424,6 +424,110 @@ __device__ inline f32x4 epi_apply4(const EpiView &v, f32x4 acc, float sa, f32x4 
 }
 
 // ---------------------------------------------------------------------------
+// Extended epilogue: z as above is also written out (pre, rounded to C's type)
+// and C = cvt(act(z) + res): the residual joins in fp32, so C is rounded once.
+// Compiled as separate kernels (EX), so the plain epilogue's code and registers
+// stay as they are.  Each lane reads the residual of exactly the elements it
+// stores, before it stores them, so res may be C itself.
+// ---------------------------------------------------------------------------
+struct EpiExt {
+    __amdgpu_buffer_rsrc_t rr, rp;   // residual and pre-activation, over the rows the tile stores
+    bool has_res, has_pre;
+};
+
+// `off` is the byte offset of the tile's first row in C, `bytes` the range its
+// rows cover (the same numbers the C resource is made of).
+__device__ inline EpiExt epi_ext(const EpiArgs &e, size_t off, uint32_t bytes)
+{
+    EpiExt x;
+    x.has_res = e.res != nullptr;
+    x.has_pre = e.pre != nullptr;
+    x.rr = make_rsrc((const uint8_t *)e.res + (x.has_res ? off : 0), x.has_res ? bytes : 0u);
+    x.rp = make_rsrc((uint8_t *)e.pre + (x.has_pre ? off : 0), x.has_pre ? bytes : 0u);
+    return x;
+}
+
+__device__ inline float bf16_lo(uint32_t w) { return as_f32(w << 16); }
+__device__ inline float bf16_hi(uint32_t w) { return as_f32(w & 0xFFFF0000u); }
+
+// z of one element without its activation.
+__device__ inline float epi_z1(const EpiView &v, float acc, float sa, float sb, float bz)
+{
+    const float z = (acc * sa) * sb;
+    return v.has_bias ? z + bz : z;
+}
+
+template <int OUT>
+__device__ inline f32x4 epi_res4(const EpiExt &x, uint32_t voff)
+{
+    if (!x.has_res)
+        return f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (OUT == kOutF32) {
+        return __builtin_bit_cast(f32x4, buf_load16(x.rr, voff, 0));
+    } else {
+        const u32x2 w = buf_load8(x.rr, voff, 0);
+        return f32x4{bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
+    }
+}
+
+template <int OUT>
+__device__ inline void epi_store4(__amdgpu_buffer_rsrc_t r, f32x4 v, uint32_t voff)
+{
+    if constexpr (OUT == kOutF32)
+        buf_store16(r, __builtin_bit_cast(u32x4, v), voff);
+    else
+        buf_store8(r, u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)}, voff);
+}
+
+// Four columns of one row: pre-activation, activation, residual, store.
+template <int OUT>
+__device__ inline void epi_finish4(const EpiView &v, const EpiExt &x, __amdgpu_buffer_rsrc_t rC, f32x4 acc, float sa,
+                                   f32x4 sb, f32x4 bz, uint32_t voff)
+{
+    const f32x4 r = epi_res4<OUT>(x, voff);
+    const f32x4 z = f32x4{epi_z1(v, acc.x, sa, sb.x, bz.x), epi_z1(v, acc.y, sa, sb.y, bz.y),
+                          epi_z1(v, acc.z, sa, sb.z, bz.z), epi_z1(v, acc.w, sa, sb.w, bz.w)};
+    if (x.has_pre)
+        epi_store4<OUT>(x.rp, z, voff);
+    f32x4 y = f32x4{epi_act(z.x, v.act), epi_act(z.y, v.act), epi_act(z.z, v.act), epi_act(z.w, v.act)};
+    if (x.has_res)
+        y += r;
+    epi_store4<OUT>(rC, y, voff);
+}
+
+// The same for two columns (s0, s1 hold the sums; on return the outputs).
+template <int OUT>
+__device__ inline void epi_finish2(const EpiView &v, const EpiExt &x, float &s0, float &s1, float sa,
+                                   const float (&sb)[2], const float (&bz)[2], uint32_t voff)
+{
+    const float z0 = epi_z1(v, s0, sa, sb[0], bz[0]), z1 = epi_z1(v, s1, sa, sb[1], bz[1]);
+    float r0 = 0.f, r1 = 0.f;
+    if (x.has_res) {
+        if constexpr (OUT == kOutF32) {
+            const u32x2 w = buf_load8(x.rr, voff, 0);
+            r0 = as_f32(w.x);
+            r1 = as_f32(w.y);
+        } else {
+            const uint32_t w = buf_load4(x.rr, voff, 0);
+            r0 = bf16_lo(w);
+            r1 = bf16_hi(w);
+        }
+    }
+    if (x.has_pre) {
+        if constexpr (OUT == kOutF32)
+            buf_store8(x.rp, u32x2{__builtin_bit_cast(uint32_t, z0), __builtin_bit_cast(uint32_t, z1)}, voff);
+        else
+            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(z0, z1), x.rp, voff, 0, 0);
+    }
+    s0 = epi_act(z0, v.act);
+    s1 = epi_act(z1, v.act);
+    if (x.has_res) {
+        s0 += r0;
+        s1 += r1;
+    }
+}
+
+// ---------------------------------------------------------------------------
 // B stored K x N (bf16): K-rows of a tile in LDS and the gfx950 transpose read.
 // ---------------------------------------------------------------------------
 // XOR applied to the 16-byte chunk index of K-row k of a K x N B tile: the 4

@@ -50,7 +50,7 @@ using dic = std::integral_constant<int, N>;
 
 }  // namespace
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX>
 __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const TiledArgs p)
 {
     static_assert(ELEM == kBf16 || ELEM == kFp8 || (ELEM == kI8 && OUT == kOutBf16),
@@ -424,6 +424,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)sk.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
+    const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
     f32x4 sbv[FN], bzv[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -440,6 +441,10 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
             const int col = n0 + wn * WTN + j * 16 + 4 * q;
             const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * OB : kOobOffset;
             const f32x4 a = I8 ? int_acc_to_f32(acc[i][j], 1.f) : acc[i][j];
+            if constexpr (EX) {
+                epi_finish4<OUT>(ev, ex, rC, a, sa, sbv[j], bzv[j], voff);
+                continue;
+            }
             const f32x4 v = epi_apply4(ev, a, sa, sbv[j], bzv[j]);
             if constexpr (OUT == kOutF32)
                 buf_store16(rC, __builtin_bit_cast(u32x4, v), voff);
@@ -449,28 +454,32 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     }
 }
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX = false>
 static hipError_t launch_dma(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_dma_kernel<ELEM, OUT, BPRE, WGM, WGN, PD, BKN, AKM>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_dma_kernel<ELEM, OUT, BPRE, WGM, WGN, PD, BKN, AKM, EX>), dim3(a.grid),
                        dim3(64 * WGM * WGN), 0, s, a);
     return hipGetLastError();
 }
 
 #define TG_DMA(ELEM, OUT, BPRE, WGM, WGN, PD)                                                       \
     TiledVariant{DM_BM, DM_BN, WGM, WGN, ELEM, OUT, BPRE, DM_LDS, 2,                                    \
-                 &launch_dma<ELEM, OUT, BPRE, WGM, WGN, PD, false, false>}
+                 &launch_dma<ELEM, OUT, BPRE, WGM, WGN, PD, false, false>, false, false,                \
+                 &launch_dma<ELEM, OUT, BPRE, WGM, WGN, PD, false, false, true>}
 #define TG_DMA_L(OUT, WGM, WGN, PD, BKN, AKM)                                                        \
     TiledVariant{DM_BM, DM_BN, WGM, WGN, kBf16, OUT, false, DM_LDS, 2,                                  \
-                 &launch_dma<kBf16, OUT, false, WGM, WGN, PD, BKN, AKM>, BKN, AKM}
+                 &launch_dma<kBf16, OUT, false, WGM, WGN, PD, BKN, AKM>, BKN, AKM,                      \
+                 &launch_dma<kBf16, OUT, false, WGM, WGN, PD, BKN, AKM, true>}
 #define TG_DMA_KN(OUT, WGM, WGN, PD) TG_DMA_L(OUT, WGM, WGN, PD, true, false)
 #define TG_DMA_KN8E(ELEM, WGM, WGN, PD)                                                            \
     TiledVariant{DM_BM, DM_BN, WGM, WGN, ELEM, kOutBf16, false, DM_LDS, 2,                              \
-                 &launch_dma<ELEM, kOutBf16, false, WGM, WGN, PD, true, false>, true, false}
+                 &launch_dma<ELEM, kOutBf16, false, WGM, WGN, PD, true, false>, true, false,            \
+                 &launch_dma<ELEM, kOutBf16, false, WGM, WGN, PD, true, false, true>}
 #define TG_DMA_KN8(WGM, WGN, PD) TG_DMA_KN8E(kFp8, WGM, WGN, PD)
 #define TG_DMA_AT8(ELEM, BKN)                                                                      \
     TiledVariant{DM_BM, DM_BN, 1, 8, ELEM, kOutBf16, false, DM_LDS, 2,                                  \
-                 &launch_dma<ELEM, kOutBf16, false, 1, 8, 2, BKN, true>, BKN, true}
+                 &launch_dma<ELEM, kOutBf16, false, 1, 8, 2, BKN, true>, BKN, true,                     \
+                 &launch_dma<ELEM, kOutBf16, false, 1, 8, 2, BKN, true, true>}
 
 static const TiledVariant kDma[] = {
     TG_DMA(kBf16, kOutBf16, false, 2, 4, 6),   // B N x K

@@ -81,7 +81,7 @@ __device__ inline void mxw(f32x16 &acc, i32x8 x, i32x8 y, uint32_t sx, uint32_t 
 
 }  // namespace
 
-template <int ELEM, bool BPRE, int WAVES, int PD>
+template <int ELEM, bool BPRE, int WAVES, int PD, bool EX>
 __global__ __launch_bounds__(64 * WAVES, 1) void gemm_mxw_kernel(const TiledArgs p)
 {
     constexpr bool F8 = ELEM == kMx8;
@@ -342,6 +342,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_mxw_kernel(const TiledArgs
     const EpiView ev = epi_view(p.epi, p.M, p.N);
     const uint32_t ldc = (uint32_t)p.N * 2u;
     const auto rC = make_rsrc((uint8_t *)sk.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
+    const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
     f32x4 sbv[JB][4], bzv[JB][4];
 #pragma unroll
     for (int J = 0; J < JB; ++J)
@@ -363,22 +364,26 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_mxw_kernel(const TiledArgs
                 const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * 2u : kOobOffset;
                 const f32x4 a = f32x4{acc[i][J][4 * u], acc[i][J][4 * u + 1], acc[i][J][4 * u + 2],
                                       acc[i][J][4 * u + 3]};
+                if constexpr (EX) {
+                    epi_finish4<kOutBf16>(ev, ex, rC, a, sa, sbv[J][u], bzv[J][u], voff);
+                    continue;
+                }
                 const f32x4 v = epi_apply4(ev, a, sa, sbv[J][u], bzv[J][u]);
                 buf_store8(rC, u32x2{pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)}, voff);
             }
     }
 }
 
-template <int ELEM, bool BPRE, int WAVES, int PD>
+template <int ELEM, bool BPRE, int WAVES, int PD, bool EX = false>
 static hipError_t launch_mxw(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_mxw_kernel<ELEM, BPRE, WAVES, PD>), dim3(a.grid), dim3(64 * WAVES), 0, s, a);
+    hipLaunchKernelGGL((gemm_mxw_kernel<ELEM, BPRE, WAVES, PD, EX>), dim3(a.grid), dim3(64 * WAVES), 0, s, a);
     return hipGetLastError();
 }
 
 #define TG_MXW(ELEM, BPRE, WAVES, PD)                                                            \
     TiledVariant{W4_BM, W4_BN, 1, WAVES, ELEM, kOutBf16, BPRE, W4_NS * W4_STAGE, W4_NS,           \
-                 &launch_mxw<ELEM, BPRE, WAVES, PD>}
+                 &launch_mxw<ELEM, BPRE, WAVES, PD>, false, false, &launch_mxw<ELEM, BPRE, WAVES, PD, true>}
 
 // The first variant of each layout is the planner's choice; the rest are
 // alternatives compiled into sweep builds only.

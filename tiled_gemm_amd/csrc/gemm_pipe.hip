@@ -70,7 +70,8 @@ using ic = std::integral_constant<int, N>;
 // BPRE: B is the pre-shuffled image (true) or plain N x K (false).
 // ADMA: A goes global -> LDS by the load's own LDS write (true) or through
 // VGPRs: loaded at barrier(k), written with ds_write_b128 at barrier(k+1).
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD,
+          bool EX>
 __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const TiledArgs p)
 {
     using Cfg = BpCfg<WGM, WGN, NS>;
@@ -484,6 +485,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)sk.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
+    const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
     f32x4 sbv[BP_FN], bzv[BP_FN];
 #pragma unroll
     for (int j = 0; j < BP_FN; ++j) {
@@ -500,6 +502,10 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
             const int col = n0 + wn * BP_WTN + j * 16 + 4 * q;
             const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * OB : kOobOffset;
             const f32x4 a = INT ? int_acc_to_f32(acc[i][j], W4 ? 0.0625f : 1.f) : acc[i][j];
+            if constexpr (EX) {
+                epi_finish4<OUT>(ev, ex, rC, a, sa, sbv[j], bzv[j], voff);
+                continue;
+            }
             const f32x4 v = epi_apply4(ev, a, sa, sbv[j], bzv[j]);
             if constexpr (OUT == kOutF32)
                 buf_store16(rC, __builtin_bit_cast(u32x4, v), voff);
@@ -509,10 +515,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
     }
 }
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD,
+          bool EX = false>
 static hipError_t launch_pipe(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_pipe_kernel<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, ACCA, SPREAD>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_pipe_kernel<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, ACCA, SPREAD, EX>), dim3(a.grid),
                        dim3(64 * WGM * WGN), 0, s, a);
     return hipGetLastError();
 }
@@ -520,17 +527,22 @@ static hipError_t launch_pipe(const TiledArgs &a, hipStream_t s)
 #define TG_PIPE_S(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, SPREAD)                              \
     TiledVariant{BP_BM, BP_BN, WGM, WGN, ELEM, OUT, BPRE, BpCfg<WGM, WGN, NS>::LDS, NS,          \
                  &launch_pipe<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, (WGM * WGN == 4), SPREAD>}
+// with the extended epilogue as well
+#define TG_PIPE_X(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, SPREAD)                              \
+    TiledVariant{BP_BM, BP_BN, WGM, WGN, ELEM, OUT, BPRE, BpCfg<WGM, WGN, NS>::LDS, NS,          \
+                 &launch_pipe<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, (WGM * WGN == 4), SPREAD>, false, false, \
+                 &launch_pipe<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, (WGM * WGN == 4), SPREAD, true>}
 #define TG_PIPE(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA) TG_PIPE_S(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, false)
 
 // The first 8-wave and the first 4-wave variant of each (elem, out, layout)
 // are the ones a plan can get; sweep builds add alternatives.
 static const TiledVariant kPipe[] = {
-    TG_PIPE_S(kBf16, kOutBf16, true, 1, 8, 4, 6, true, true),
-    TG_PIPE_S(kBf16, kOutF32, true, 1, 8, 4, 6, true, true),
+    TG_PIPE_X(kBf16, kOutBf16, true, 1, 8, 4, 6, true, true),
+    TG_PIPE_X(kBf16, kOutF32, true, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kBf16, kOutBf16, false, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kBf16, kOutF32, false, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kFp8, kOutBf16, false, 1, 8, 4, 3, true, true),
-    TG_PIPE_S(kFp8, kOutBf16, true, 1, 8, 4, 3, true, true),
+    TG_PIPE_X(kFp8, kOutBf16, true, 1, 8, 4, 3, true, true),
     // 4 waves, one per SIMD, 256 accumulators each in AGPRs
     TG_PIPE_S(kBf16, kOutBf16, true, 1, 4, 4, 12, true, true),
     TG_PIPE_S(kBf16, kOutBf16, false, 1, 4, 4, 12, true, true),
@@ -544,10 +556,10 @@ static const TiledVariant kPipe[] = {
     TG_PIPE_S(kMx4, kOutBf16, true, 1, 4, 4, 12, true, true),
     TG_PIPE_S(kMx4, kOutBf16, false, 1, 4, 4, 12, true, true),
     // integer operands: 8 waves, then 4 waves with AGPR accumulators
-    TG_PIPE_S(kI8, kOutBf16, true, 1, 8, 4, 6, true, true),     // 16
+    TG_PIPE_X(kI8, kOutBf16, true, 1, 8, 4, 6, true, true),     // 16
     TG_PIPE_S(kI8, kOutBf16, false, 1, 8, 4, 6, true, true),
-    TG_PIPE_S(kW4A8, kOutBf16, true, 1, 8, 4, 6, true, true),
-    TG_PIPE_S(kW4A8, kOutBf16, false, 1, 8, 4, 6, true, true),
+    TG_PIPE_X(kW4A8, kOutBf16, true, 1, 8, 4, 6, true, true),
+    TG_PIPE_X(kW4A8, kOutBf16, false, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kI8, kOutBf16, true, 1, 4, 4, 12, true, true),    // 20
     TG_PIPE_S(kI8, kOutBf16, false, 1, 4, 4, 12, true, true),
     TG_PIPE_S(kW4A8, kOutBf16, true, 1, 4, 4, 12, true, true),

@@ -39,7 +39,7 @@ constexpr int kRedPitch = kSkinnyTileN + 1;   // padded reduction row (bank spre
 // IUNIT = 0: fp32 accumulators.  Otherwise the accumulators hold int32 sums
 // (integer MFMAs): the waves' partials are summed in int32 (exact), then
 // converted to fp32 and multiplied by 1 / IUNIT (a power of two, exact).
-template <int MB, int OUT, int WAVES, int IUNIT = 0>
+template <int MB, int OUT, int WAVES, int IUNIT = 0, bool EX = false>
 __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB][kSkinnyTileN / 16], uint8_t *lds,
                                      int n0)
 {
@@ -63,6 +63,7 @@ __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB]
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc(p.C, (uint32_t)p.M * ldc);
+    const EpiExt ex = EX ? epi_ext(p.epi, 0, (uint32_t)p.M * ldc) : EpiExt{};
     // Each thread finishes pairs of adjacent outputs.
     for (int o = threadIdx.x * 2; o < ROWS_A * kSkinnyTileN; o += 64 * WAVES * 2) {
         const int row = o / kSkinnyTileN, col = o % kSkinnyTileN;
@@ -87,9 +88,13 @@ __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB]
         float sb[2], bz[2];
         epi_col2(ev, n, sb, bz);
         const float sa = epi_row_scale(ev, row);
-        s0 = epi_apply1(ev, s0, sa, sb[0], bz[0]);
-        s1 = epi_apply1(ev, s1, sa, sb[1], bz[1]);
         const uint32_t voffc = (row < p.M && n < p.N) ? (uint32_t)row * ldc + (uint32_t)n * OB : kOobOffset;
+        if constexpr (EX)
+            epi_finish2<OUT>(ev, ex, s0, s1, sa, sb, bz, voffc);
+        else {
+            s0 = epi_apply1(ev, s0, sa, sb[0], bz[0]);
+            s1 = epi_apply1(ev, s1, sa, sb[1], bz[1]);
+        }
         if constexpr (OUT == kOutF32)
             __builtin_amdgcn_raw_buffer_store_b64(u32x2{__builtin_bit_cast(uint32_t, s0),
                                                         __builtin_bit_cast(uint32_t, s1)},
@@ -113,7 +118,7 @@ struct SkinnyCfg {
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX>
 __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const SkinnyArgs p)
 {
     using Cfg = SkinnyCfg<MB, WAVES, DEPTH>;
@@ -230,13 +235,13 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const Skinny
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);
     __syncthreads();
 
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : 0>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : 0, EX>(p, acc, lds, n0);
 }
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX = false>
 static hipError_t launch_skinny(const SkinnyArgs &a, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_skinny_kernel<MB, ELEM, OUT, WAVES, DEPTH, ROTATE>), dim3(grid), dim3(64 * WAVES), 0,
+    hipLaunchKernelGGL((gemm_skinny_kernel<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, EX>), dim3(grid), dim3(64 * WAVES), 0,
                        s, a);
     return hipGetLastError();
 }
@@ -266,7 +271,7 @@ struct SkinnyPreCfg {
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX>
 __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const SkinnyArgs p)
 {
     // Packed int4 B (W4A8): one 1 KiB block per 16 columns and step, i.e. the
@@ -465,24 +470,26 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     if constexpr (MX)
         mfma_drain_acc(acc);                      // the scaled MFMAs are inline assembly
     __syncthreads();
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : (W4 ? 16 : 0)>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : (W4 ? 16 : 0), EX>(p, acc, lds, n0);
 }
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX = false>
 static hipError_t launch_skinny_pre(const SkinnyArgs &a, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_skinny_pre_kernel<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD>), dim3(grid), dim3(64 * WAVES), 0,
+    hipLaunchKernelGGL((gemm_skinny_pre_kernel<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, EX>), dim3(grid), dim3(64 * WAVES), 0,
                        s, a);
     return hipGetLastError();
 }
 
 #define TG_SKINNY(MB, ELEM, OUT, WAVES, DEPTH, ROTATE)                                                       \
     SkinnyVariant{MB, ELEM, OUT, WAVES, DEPTH, SkinnyCfg<MB, WAVES, DEPTH>::LDS,                             \
-                  &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE>}
+                  &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE>, false,                                \
+                  &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, true>}
 
 #define TG_SKINNY_PRE_O(MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD)                                              \
     SkinnyVariant{MB, ELEM, OUT, WAVES, DEPTH, SkinnyPreCfg<MB, WAVES, DEPTH, BLDS, ELEM == kW4A8 ? 1 : 2>::LDS, \
-                  &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD>, true}
+                  &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD>, true,                           \
+                  &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, true>}
 #define TG_SKINNY_PRE_L(MB, ELEM, OUT, WAVES, DEPTH, BLDS) TG_SKINNY_PRE_O(MB, ELEM, OUT, WAVES, DEPTH, BLDS, 1)
 #define TG_SKINNY_PRE(MB, ELEM, OUT, WAVES, DEPTH) TG_SKINNY_PRE_L(MB, ELEM, OUT, WAVES, DEPTH, false)
 

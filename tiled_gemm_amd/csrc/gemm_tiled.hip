@@ -60,7 +60,7 @@ struct TiledCfg {
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
 };
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN>
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX>
 __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p)
 {
     using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>;
@@ -278,6 +278,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
+    const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
     // Row blocks outside, column blocks inside: adjacent pieces of a C row
     // leave back to back and merge in the L2 into whole lines.
 #pragma unroll
@@ -288,6 +289,10 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
         for (int j = 0; j < FN; ++j) {
             const int col = n0 + wn * Cfg::WTN + j * 16 + 4 * q;
             const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * OB : kOobOffset;
+            if constexpr (EX) {
+                epi_finish4<OUT>(ev, ex, rC, acc[i][j], sa, epi_col_scale4(ev, col), epi_bias4(ev, col), voff);
+                continue;
+            }
             const f32x4 v = epi_apply4(ev, acc[i][j], sa, epi_col_scale4(ev, col), epi_bias4(ev, col));
             if constexpr (OUT == kOutF32) {
                 buf_store16(rC, __builtin_bit_cast(u32x4, v), voff);
@@ -298,10 +303,10 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN>
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX = false>
 static hipError_t launch_tiled(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, EX>), dim3(a.grid),
                        dim3(kTiledThreads), 0, s, a);
     return hipGetLastError();
 }
@@ -310,6 +315,12 @@ static hipError_t launch_tiled(const TiledArgs &a, hipStream_t s)
     TiledVariant{BM, BN, WGM, WGN, ELEM, OUT, BPRE,                                         \
                  TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>::LDS, 2,                  \
                  &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>, BKN}
+// the planner's own 128 x 128 tiles, with the extended epilogue as well
+#define TG_TILED_X(BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN)                                 \
+    TiledVariant{BM, BN, WGM, WGN, ELEM, OUT, BPRE,                                         \
+                 TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>::LDS, 2,                  \
+                 &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>, BKN, false,          \
+                 &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, true>}
 #define TG_TILED(BM, BN, WGM, WGN, ELEM, BPRE, OUT) TG_TILED_L(BM, BN, WGM, WGN, ELEM, BPRE, OUT, false)
 
 static const TiledVariant kTiled[] = {
@@ -319,17 +330,17 @@ static const TiledVariant kTiled[] = {
     TG_TILED(256, 256, 1, 4, kBf16, true, kOutF32),
     TG_TILED(256, 256, 2, 2, kFp8, false, kOutBf16),
     TG_TILED(256, 256, 1, 4, kFp8, true, kOutBf16),
-    TG_TILED(128, 128, 2, 2, kBf16, false, kOutBf16),
-    TG_TILED(128, 128, 2, 2, kBf16, false, kOutF32),
-    TG_TILED(128, 128, 2, 2, kBf16, true, kOutBf16),
-    TG_TILED(128, 128, 2, 2, kBf16, true, kOutF32),
-    TG_TILED(128, 128, 2, 2, kFp8, false, kOutBf16),
-    TG_TILED(128, 128, 2, 2, kFp8, true, kOutBf16),
+    TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutBf16, false),
+    TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutF32, false),
+    TG_TILED_X(128, 128, 2, 2, kBf16, true, kOutBf16, false),
+    TG_TILED_X(128, 128, 2, 2, kBf16, true, kOutF32, false),
+    TG_TILED_X(128, 128, 2, 2, kFp8, false, kOutBf16, false),
+    TG_TILED_X(128, 128, 2, 2, kFp8, true, kOutBf16, false),
     // B stored K x N (bf16)
     TG_TILED_L(256, 256, 2, 2, kBf16, false, kOutBf16, true),
     TG_TILED_L(256, 256, 2, 2, kBf16, false, kOutF32, true),
-    TG_TILED_L(128, 128, 2, 2, kBf16, false, kOutBf16, true),
-    TG_TILED_L(128, 128, 2, 2, kBf16, false, kOutF32, true),
+    TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutBf16, true),
+    TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutF32, true),
 };
 
 const TiledVariant *tiled_variants(int *count)

@@ -14,7 +14,9 @@ namespace tg {
 enum Elem { kBf16 = 0, kFp8 = 1, kMx8 = 2, kMx4 = 3, kI8 = 4, kW4A8 = 5 };
 enum Out { kOutF32 = 0, kOutBf16 = 1 };
 
-// Epilogue operands (device pointers): C = act((acc * s_a) * s_b + bias).
+// Epilogue operands (device pointers): C = act((acc * s_a) * s_b + bias), and
+// in the extended epilogue (the variants' launch_ex) + res, with the
+// pre-activation also written to pre.
 enum EpiAct { kActNone = 0, kActRelu = 1, kActSilu = 2, kActGelu = 3 };
 struct EpiArgs {
     const float *sa;        // nullptr (1), one value for every row, or one per row of C
@@ -23,6 +25,8 @@ struct EpiArgs {
     int32_t sa_rows;        // 0: sa[0] for every row; 1: sa[row]
     int32_t sb_cols;        // 0: sb[0] for every column; 1: sb[col]
     int32_t act;            // EpiAct
+    const void *res;        // launch_ex: nullptr (0) or M x N of C's type, may be C itself
+    void *pre;              // launch_ex: nullptr or M x N of C's type
 };
 
 struct TiledArgs {
@@ -62,6 +66,7 @@ struct SplitReduceArgs {
     int32_t M, N;
     int32_t splits;
     int32_t out;            // kOutF32 or kOutBf16
+    bool ex;                // extended epilogue (epi.res, epi.pre)
 };
 
 // Block-scale image of an MX operand with R rows: the bytes
@@ -122,6 +127,9 @@ struct TiledVariant {
     hipError_t (*launch)(const TiledArgs &, hipStream_t);
     bool bkn = false;       // B stored K x N
     bool akm = false;       // A stored K x M
+    // The kernel with the extended epilogue (residual, saved pre-activation):
+    // present for every variant a plan with the planner's own choice can get.
+    hipError_t (*launch_ex)(const TiledArgs &, hipStream_t) = nullptr;
 };
 
 struct SkinnyVariant {
@@ -132,6 +140,7 @@ struct SkinnyVariant {
     int lds_bytes;
     hipError_t (*launch)(const SkinnyArgs &, int grid, hipStream_t);
     bool preshuffled = false;   // B is the pre-shuffled image (register-staged B)
+    hipError_t (*launch_ex)(const SkinnyArgs &, int grid, hipStream_t) = nullptr;   // extended epilogue
 };
 
 constexpr int kSkinnyTileN = 32;

@@ -22,6 +22,40 @@ constexpr int kReduceThreads = 256;
 constexpr int kReduceCols = 8;           // columns per thread
 
 template <int OUT>
+__device__ inline void store_cols(void *base, size_t at, const float (&v)[kReduceCols])
+{
+    if constexpr (OUT == kOutF32) {
+        float *c = (float *)base + at;
+        *(f32x4 *)c = f32x4{v[0], v[1], v[2], v[3]};
+        *(f32x4 *)(c + 4) = f32x4{v[4], v[5], v[6], v[7]};
+    } else {
+        *(u32x4 *)((uint16_t *)base + at) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    }
+}
+
+template <int OUT>
+__device__ inline void load_cols(const void *base, size_t at, float (&r)[kReduceCols])
+{
+    if constexpr (OUT == kOutF32) {
+        const float *c = (const float *)base + at;
+        const f32x4 lo = *(const f32x4 *)c, hi = *(const f32x4 *)(c + 4);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            r[t] = lo[t];
+            r[4 + t] = hi[t];
+        }
+    } else {
+        const u32x4 w = *(const u32x4 *)((const uint16_t *)base + at);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            r[2 * t] = bf16_lo(w[t]);
+            r[2 * t + 1] = bf16_hi(w[t]);
+        }
+    }
+}
+
+template <int OUT, bool EX>
 __global__ __launch_bounds__(kReduceThreads) void split_reduce_kernel(const SplitReduceArgs a)
 {
     const size_t per_row = (size_t)a.N / kReduceCols;
@@ -46,28 +80,45 @@ __global__ __launch_bounds__(kReduceThreads) void split_reduce_kernel(const Spli
     for (int t = 0; t < kReduceCols; t += 2) {
         float sb[2], bz[2];
         epi_col2(ev, col + t, sb, bz);
-        v[t] = epi_apply1(ev, v[t], sa, sb[0], bz[0]);
-        v[t + 1] = epi_apply1(ev, v[t + 1], sa, sb[1], bz[1]);
+        if constexpr (EX) {
+            v[t] = epi_z1(ev, v[t], sa, sb[0], bz[0]);
+            v[t + 1] = epi_z1(ev, v[t + 1], sa, sb[1], bz[1]);
+        } else {
+            v[t] = epi_apply1(ev, v[t], sa, sb[0], bz[0]);
+            v[t + 1] = epi_apply1(ev, v[t + 1], sa, sb[1], bz[1]);
+        }
     }
-    if constexpr (OUT == kOutF32) {
-        float *c = (float *)a.C + (size_t)row * a.N + col;
-        *(f32x4 *)c = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4 *)(c + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-        uint16_t *c = (uint16_t *)a.C + (size_t)row * a.N + col;
-        *(u32x4 *)c = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                            pack_bf16x2(v[6], v[7])};
+    const size_t at = (size_t)row * a.N + col;
+    if constexpr (EX) {
+        // v holds z; the residual is read before C is stored (it may be C)
+        float r[kReduceCols] = {};
+        if (a.epi.res)
+            load_cols<OUT>(a.epi.res, at, r);
+        if (a.epi.pre)
+            store_cols<OUT>(a.epi.pre, at, v);
+#pragma unroll
+        for (int t = 0; t < kReduceCols; ++t) {
+            v[t] = epi_act(v[t], ev.act);
+            if (a.epi.res)
+                v[t] += r[t];
+        }
     }
+    store_cols<OUT>(a.C, at, v);
 }
 
 hipError_t launch_split_reduce(const SplitReduceArgs &a, hipStream_t s)
 {
     const size_t items = (size_t)a.M * (size_t)(a.N / kReduceCols);
     const size_t blocks = (items + kReduceThreads - 1) / kReduceThreads;
-    if (a.out == kOutF32)
-        hipLaunchKernelGGL(split_reduce_kernel<kOutF32>, dim3((unsigned)blocks), dim3(kReduceThreads), 0, s, a);
+    const dim3 grid((unsigned)blocks), threads(kReduceThreads);
+    if (a.out == kOutF32 && a.ex)
+        hipLaunchKernelGGL((split_reduce_kernel<kOutF32, true>), grid, threads, 0, s, a);
+    else if (a.out == kOutF32)
+        hipLaunchKernelGGL((split_reduce_kernel<kOutF32, false>), grid, threads, 0, s, a);
+    else if (a.ex)
+        hipLaunchKernelGGL((split_reduce_kernel<kOutBf16, true>), grid, threads, 0, s, a);
     else
-        hipLaunchKernelGGL(split_reduce_kernel<kOutBf16>, dim3((unsigned)blocks), dim3(kReduceThreads), 0, s, a);
+        hipLaunchKernelGGL((split_reduce_kernel<kOutBf16, false>), grid, threads, 0, s, a);
     return hipGetLastError();
 }
 
