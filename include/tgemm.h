@@ -287,6 +287,7 @@ int gemm_run_ws(const gemm_plan *plan, const void *A, const void *B, void *C,
  *             must not overlap C.
  *   preact    device pointer, M x N of C's type, 16-byte aligned, or NULL.
  *             Must not overlap A, B, C, the residual or the workspace.
+ *             gemm_act_grad takes it for the backward pass.
  *   workspace, workspace_bytes  as for gemm_run_ws (NULL, 0: no split).  It
  *             must not overlap the residual either.
  * Plans with GEMM_KERNEL_AUTO or GEMM_KERNEL_TILE256; the other explicit
@@ -405,6 +406,203 @@ int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, 
  * products (each at most 2^14 in magnitude) can leave the int32 range.
  * Run through gemm_run or gemm_run_ex.
  */
+
+/* ------------------------------------------------------------------------
+ * Products grouped by expert.  A mixture-of-experts layer sends every token to
+ * a few of G experts; the rows that go to one expert form a group, and each
+ * group is multiplied by its own B.  The groups' sizes are only known on the
+ * device: they are given as G + 1 offsets in device memory, group g holding
+ * the rows offsets[g] .. offsets[g + 1] - 1, and no call reads them on the host.
+ * The usual chain is
+ *
+ *   gemm_group_sort     expert ids -> offsets, row_token, slot_row
+ *   gemm_group_run      up projection (row_index = row_token gathers the tokens)
+ *   gemm_group_run      down projection
+ *   gemm_group_combine  the weighted sum of each token's rows (slot_row)
+ *
+ * and backwards gemm_group_combine_grad, gemm_act_grad, gemm_group_run with
+ * GEMM_LAYOUT_BN (input gradients) and GEMM_LAYOUT_AT_BN (weight gradients),
+ * and gemm_group_combine without weights (the gradient of the gather).
+ * ------------------------------------------------------------------------ */
+#define GEMM_GROUP_MAX 1024                 /* most groups                            */
+#define GEMM_GROUP_MAX_ROWS ((int64_t)1 << 24)   /* most rows (or slots) of one call */
+
+typedef enum {
+    GEMM_TYPE_F32 = 0,
+    GEMM_TYPE_BF16 = 1
+} gemm_type;
+
+typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after creation */
+
+/*
+ * gemm_group_plan_create -- validate a grouped product and pick its kernel.
+ *   groups   G, 1 .. GEMM_GROUP_MAX.
+ *   M, N, K, dtype, layout  as for gemm_plan_create, with:
+ *     GEMM_LAYOUT_BT, GEMM_LAYOUT_BT_PRESHUFFLED, GEMM_LAYOUT_BN (bf16): the
+ *       ROWS are grouped.  A is M x K and C is M x N, M being the number of
+ *       rows they have room for (offsets[G] may be less); B is G matrices,
+ *       N x K each (BN: K x N each), one behind the other.  Row r of group g:
+ *           C[r] = cvt( epilogue( A[r] * B_g^T ) )     (BN: A[r] * B_g)
+ *     GEMM_LAYOUT_AT_BN (bf16): the INNER size is grouped.  A is K x M and B
+ *       is K x N, K being the number of rows they have room for; C is G
+ *       matrices M x N.  Every matrix of C is written, zeros for an empty
+ *       group:
+ *           C_g = cvt( sum over rows r of group g of A[r]^T * B[r] )
+ *       K may be any number here; M * 2 % 16 == 0.
+ *   dtype    GEMM_BF16_OUT_F32, GEMM_BF16_OUT_BF16, GEMM_E4M3_OUT_BF16 (the
+ *            last with GEMM_LAYOUT_BT and GEMM_LAYOUT_BT_PRESHUFFLED).
+ * The other requirements are gemm_plan_create's (N % 16 == 0; K * elem_bytes
+ * % 64 == 0 where rows are grouped; ...); grouped rows at most
+ * GEMM_GROUP_MAX_ROWS.  Host only.  NULL on error; freed with
+ * gemm_group_plan_destroy.
+ */
+gemm_group_plan *gemm_group_plan_create(int groups, int64_t M, int64_t N, int64_t K, int dtype, int layout);
+
+/*
+ * gemm_group_plan_create_opt -- the same with the kernel family named by the
+ * rows of its tiles: 16, 32 or 64 (skinny kernels, GEMM_LAYOUT_BT and
+ * GEMM_LAYOUT_BT_PRESHUFFLED), 128 (not GEMM_LAYOUT_AT_BN) or 256; 0 the
+ * planner's own choice from M / groups.  Every choice computes the same C
+ * within the same bound.  GEMM_ERR_UNSUPPORTED when the family has no kernel
+ * for the dtype and layout.
+ */
+gemm_group_plan *gemm_group_plan_create_opt(int groups, int64_t M, int64_t N, int64_t K, int dtype, int layout,
+                                            int tile_rows);
+void gemm_group_plan_destroy(gemm_group_plan *plan);
+
+typedef struct {
+    int64_t M, N, K;
+    int32_t groups, dtype, layout;
+    int32_t kernel;          /* 0 tiled, 1 skinny                                     */
+    int32_t tile_m, tile_n;
+    int32_t threads, lds_bytes;
+    int32_t grid;            /* workgroups of one launch (an upper bound on the tiles) */
+} gemm_group_plan_info;
+int gemm_group_plan_query(const gemm_group_plan *plan, gemm_group_plan_info *info);
+
+/*
+ * gemm_group_preshuffled_b_bytes, gemm_group_preshuffle_b -- the pre-shuffled
+ * images of the G matrices B, one behind the other (gemm_preshuffle_b on
+ * each).  Arguments and errors as there; 0 bytes for the layouts without an
+ * image.
+ */
+size_t gemm_group_preshuffled_b_bytes(const gemm_group_plan *plan);
+int gemm_group_preshuffle_b(const gemm_group_plan *plan, const void *B, void *B_shuf, hipStream_t stream);
+
+/*
+ * gemm_group_run -- the grouped product on `stream`.
+ *   A, B, C    device pointers, 16-byte aligned, as described above.
+ *   offsets    device pointer, G + 1 ints, not decreasing, 0 <= offsets[0],
+ *              offsets[G] <= M (AT_BN: K).  Values outside are clamped to that
+ *              range; rows of C outside every group are left as they were.
+ *              Each row may belong to one group only.
+ *   row_index  device pointer to M ints, or NULL.  Given, A has a_rows rows and
+ *              row r of C is made from row row_index[r] of A (the gather of the
+ *              tokens, without a copy); an index outside 0 .. a_rows - 1 stands
+ *              for a row of zeros.  a_rows * K * elem_bytes < 2^31.  Not for
+ *              GEMM_LAYOUT_AT_BN.
+ *   a_rows     rows of A when row_index is given (ignored otherwise).
+ *   epi        the fused epilogue, or NULL: scale_a one value or one per row of
+ *              A; scale_b one value, or G x N values (per column of every
+ *              group); bias G x N values.  AT_BN: NULL or scales of one value
+ *              and GEMM_EPI_NONE.
+ *   preact     device pointer, M x N of C's type, 16-byte aligned, or NULL: the
+ *              pre-activation, as for gemm_run_res.  Not for AT_BN.
+ * Asynchronous; allocates nothing; one launch.  Errors as gemm_run_ex.
+ */
+int gemm_group_run(const gemm_group_plan *plan, const void *A, const void *B, void *C, const int32_t *offsets,
+                   const int32_t *row_index, int64_t a_rows, const gemm_epilogue_args *epi, void *preact,
+                   hipStream_t stream);
+
+/*
+ * gemm_group_sort -- the tables of the grouped calls from the experts' ids.
+ *   ids        device pointer, `slots` ints: slot s = token * topk + j holds
+ *              the j-th expert of the token.  An id outside 0 .. groups - 1 is
+ *              a slot that goes nowhere (an expert of another rank, padding).
+ *   slots      number of ids, at most GEMM_GROUP_MAX_ROWS, a multiple of topk.
+ *   offsets    groups + 1 ints out: where each group's rows start.
+ *   row_token  `slots` ints out: the token (s / topk) of every sorted row; the
+ *              entries from offsets[groups] on are left as they were.
+ *   slot_row   `slots` ints out: the sorted row of every slot, -1 for a slot
+ *              that goes nowhere.
+ * The rows of a group keep the order of their slots (a stable sort, so the
+ * result is the same on every run).
+ *   workspace  gemm_group_sort_workspace_bytes(slots, groups) bytes of device
+ *              memory, 4-byte aligned, contents undefined before and after;
+ *              NULL when that is 0.  Calls that share one must not overlap in
+ *              time.
+ * The outputs overlap neither each other nor the ids or the workspace.
+ * Asynchronous; allocates nothing.  GEMM_OK or an error.
+ */
+size_t gemm_group_sort_workspace_bytes(int64_t slots, int groups);
+int gemm_group_sort(const int32_t *ids, int64_t slots, int topk, int groups, int32_t *offsets, int32_t *row_token,
+                    int32_t *slot_row, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * gemm_group_combine -- every token's rows brought back together:
+ *
+ *   out[t][n] = cvt( sum over j of weights[t][j] * src[slot_row[t][j]][n]  (+ residual[t][n]) )
+ *
+ * summed in fp32 in the order of j, the residual last.  A slot_row outside
+ * 0 .. src_rows - 1 contributes nothing (its weight is not read as a factor:
+ * an infinite or NaN weight of such a slot does not reach the output).
+ *   tokens, topk  0 .. GEMM_GROUP_MAX_ROWS tokens, 1 .. 64 slots per token;
+ *                 N % 16 == 0.
+ *   type       gemm_type of src, residual and out.
+ *   src        src_rows x N;  slot_row  tokens x topk ints;
+ *   weights    tokens x topk floats, or NULL (1);
+ *   residual   tokens x N or NULL; may be out itself, else no overlap;
+ *   out        tokens x N, not overlapping src.
+ * src, residual and out 16-byte aligned.  Asynchronous; GEMM_OK or an error.
+ */
+int gemm_group_combine(int64_t tokens, int topk, int64_t N, int type, const void *src, int64_t src_rows,
+                       const int32_t *slot_row, const float *weights, const void *residual, void *out,
+                       hipStream_t stream);
+
+/*
+ * gemm_group_combine_grad -- the gradient of that sum:
+ *
+ *   d_src[slot_row[t][j]][n] = cvt( weights[t][j] * d_out[t][n] )
+ *   d_weights[t][j] = sum over n of d_out[t][n] * src[slot_row[t][j]][n]     (0 for a slot that goes nowhere)
+ *
+ * Every row may be named by one slot only (as gemm_group_sort's table does);
+ * rows of d_src that no slot names are left as they were.  d_weights is fp32
+ * or NULL (src may then be NULL too); weights NULL stands for 1.  d_src does
+ * not overlap src or d_out.  The residual's gradient is d_out itself.
+ * Otherwise as gemm_group_combine.
+ */
+int gemm_group_combine_grad(int64_t tokens, int topk, int64_t N, int type, const void *d_out, const void *src,
+                            int64_t src_rows, const int32_t *slot_row, const float *weights, void *d_src,
+                            float *d_weights, hipStream_t stream);
+
+/*
+ * gemm_act_grad -- the gradient of the fused epilogue, from the saved
+ * pre-activation z (gemm_run_res, gemm_group_run):
+ *
+ *   d_z[m][n] = cvt( d_c[m][n] * act'(z[m][n]) )
+ *   d_bias[g][n] = sum over the rows m of group g of d_c[m][n] * act'(z[m][n])     (fp32, before the rounding)
+ *
+ *   act': 1; ReLU z > 0; SiLU s(z) (1 + z (1 - s(z))), s the logistic function;
+ *   GELU Phi(z) + z phi(z).  0 is taken where z is -inf (SiLU, GELU).
+ *   M, N       rows and columns (N % 16 == 0, M <= GEMM_GROUP_MAX_ROWS).
+ *   type       gemm_type of d_c, z and d_z (16-byte aligned).
+ *   epilogue   gemm_epilogue: which activation (NONE and BIAS: none).
+ *   z          M x N; may be NULL without an activation.
+ *   d_z        M x N; may be d_c or z itself, else no overlap with them.
+ *   d_bias     groups x N floats, 16-byte aligned, or NULL.
+ *   groups, offsets  the row groups (G + 1 device ints, as for
+ *              gemm_group_run); offsets NULL: one group of M rows (groups is
+ *              then 1).  Rows outside every group: d_z is left as it was.
+ *   workspace  gemm_act_grad_workspace_bytes(M, N, groups) bytes when d_bias is
+ *              given (16-byte aligned, contents undefined before and after);
+ *              not read otherwise.
+ * d_bias is summed in a fixed order (no atomics): the same on every run.
+ * Asynchronous; allocates nothing.  GEMM_OK or an error.
+ */
+size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t N, int groups);
+int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *z, void *d_z,
+                  float *d_bias, int groups, const int32_t *offsets, void *workspace, size_t workspace_bytes,
+                  hipStream_t stream);
 
 /* gemm_last_error -- message for the calling thread's last failure ("" if none). */
 const char *gemm_last_error(void);

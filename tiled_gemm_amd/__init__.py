@@ -55,9 +55,17 @@ EXPORTS = (
     "gemm_last_error", "gemm_plan_query", "gemm_plan_layout", "gemm_layout_crd2idx",
     "gemm_layout_idx2crd", "gemm_lds_swizzle", "gemm_tile_of_workgroup", "gemm_workspace_bytes",
     "gemm_run_ws", "gemm_run_ws_noalloc", "gemm_run_res", "gemm_run_mx_res",
+    "gemm_group_plan_create", "gemm_group_plan_create_opt", "gemm_group_plan_destroy", "gemm_group_plan_query",
+    "gemm_group_preshuffled_b_bytes", "gemm_group_preshuffle_b", "gemm_group_run", "gemm_group_sort_workspace_bytes",
+    "gemm_group_sort", "gemm_group_combine", "gemm_group_combine_grad", "gemm_act_grad_workspace_bytes",
+    "gemm_act_grad",
 )
 
 GEMM_STATIC_WORKSPACE_BYTES = 64 << 20
+
+GEMM_GROUP_MAX = 1024
+GEMM_GROUP_MAX_ROWS = 1 << 24
+GEMM_TYPE_F32, GEMM_TYPE_BF16 = range(2)
 
 
 class GemmError(RuntimeError):
@@ -82,6 +90,15 @@ class gemm_plan_info(ctypes.Structure):
             "dtype", "layout", "elem_bytes", "out_bytes", "kernel", "tile_m", "tile_n",
             "tile_k_bytes", "threads", "lds_stages", "lds_bytes", "grid", "tiles_m", "tiles_n",
             "group_m", "split_k", "elem_bits", "b_elem_bits", "ws_splits", "ws_grid", "scale_form")]
+
+    def as_dict(self) -> dict:
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class gemm_group_plan_info(ctypes.Structure):
+    _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("groups", "dtype", "layout", "kernel", "tile_m", "tile_n", "threads",
+                                      "lds_bytes", "grid")]
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}
@@ -118,6 +135,19 @@ def load() -> ctypes.CDLL:
         "gemm_run_ws_noalloc": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp]),
         "gemm_run_res": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp, vp, vp, ctypes.c_size_t, vp]),
         "gemm_run_mx_res": (c_int, [vp, vp, vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp, vp, vp]),
+        "gemm_group_plan_create": (vp, [c_int, i64, i64, i64, c_int, c_int]),
+        "gemm_group_plan_create_opt": (vp, [c_int, i64, i64, i64, c_int, c_int, c_int]),
+        "gemm_group_plan_destroy": (None, [vp]),
+        "gemm_group_plan_query": (c_int, [vp, ctypes.POINTER(gemm_group_plan_info)]),
+        "gemm_group_preshuffled_b_bytes": (ctypes.c_size_t, [vp]),
+        "gemm_group_preshuffle_b": (c_int, [vp, vp, vp, vp]),
+        "gemm_group_run": (c_int, [vp, vp, vp, vp, vp, vp, i64, ctypes.POINTER(gemm_epilogue_args), vp, vp]),
+        "gemm_group_sort_workspace_bytes": (ctypes.c_size_t, [i64, c_int]),
+        "gemm_group_sort": (c_int, [vp, i64, c_int, c_int, vp, vp, vp, vp, ctypes.c_size_t, vp]),
+        "gemm_group_combine": (c_int, [i64, c_int, i64, c_int, vp, i64, vp, vp, vp, vp, vp]),
+        "gemm_group_combine_grad": (c_int, [i64, c_int, i64, c_int, vp, vp, i64, vp, vp, vp, vp, vp]),
+        "gemm_act_grad_workspace_bytes": (ctypes.c_size_t, [i64, i64, c_int]),
+        "gemm_act_grad": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp, c_int, vp, vp, ctypes.c_size_t, vp]),
         "gemm_last_error": (ctypes.c_char_p, []),
         "gemm_plan_query": (c_int, [vp, ctypes.POINTER(gemm_plan_info)]),
         "gemm_plan_layout": (c_int, [vp, c_int, p32, p64, p64]),
@@ -249,6 +279,83 @@ def gemm_run_mx_res(plan: int, A: int, A_bscale: int, B: int, B_bscale: int, C: 
                                   preact or None, stream), "gemm_run_mx_res")
 
 
+def gemm_group_plan_create(groups: int, M: int, N: int, K: int, dtype: int, layout: int) -> int:
+    h = load().gemm_group_plan_create(groups, M, N, K, dtype, layout)
+    if not h:
+        raise GemmError(-1, "gemm_group_plan_create", gemm_last_error())
+    return h
+
+
+def gemm_group_plan_create_opt(groups: int, M: int, N: int, K: int, dtype: int, layout: int, tile_rows: int) -> int:
+    h = load().gemm_group_plan_create_opt(groups, M, N, K, dtype, layout, tile_rows)
+    if not h:
+        raise GemmError(-1, "gemm_group_plan_create_opt", gemm_last_error())
+    return h
+
+
+def gemm_group_plan_destroy(plan: int) -> None:
+    load().gemm_group_plan_destroy(plan)
+
+
+def gemm_group_plan_query(plan: int) -> dict:
+    info = gemm_group_plan_info()
+    _check(load().gemm_group_plan_query(plan, ctypes.byref(info)), "gemm_group_plan_query")
+    return info.as_dict()
+
+
+def gemm_group_preshuffled_b_bytes(plan: int) -> int:
+    return int(load().gemm_group_preshuffled_b_bytes(plan))
+
+
+def gemm_group_preshuffle_b(plan: int, B: int, B_shuf: int, stream: int = 0) -> None:
+    _check(load().gemm_group_preshuffle_b(plan, B, B_shuf, stream), "gemm_group_preshuffle_b")
+
+
+def gemm_group_run(plan: int, A: int, B: int, C: int, offsets: int, row_index: int | None = None, a_rows: int = 0,
+                   preact: int | None = None, scale_a: int | None = None, scale_a_per_row: bool = False,
+                   scale_b: int | None = None, scale_b_per_col: bool = False, bias: int | None = None,
+                   epilogue: int = GEMM_EPI_NONE, stream: int = 0) -> None:
+    epi = gemm_epilogue_args(scale_a or None, scale_b or None, bias or None, int(scale_a_per_row),
+                             int(scale_b_per_col), epilogue)
+    _check(load().gemm_group_run(plan, A, B, C, offsets, row_index or None, a_rows, ctypes.byref(epi),
+                                 preact or None, stream), "gemm_group_run")
+
+
+def gemm_group_sort_workspace_bytes(slots: int, groups: int) -> int:
+    return int(load().gemm_group_sort_workspace_bytes(slots, groups))
+
+
+def gemm_group_sort(ids: int, slots: int, topk: int, groups: int, offsets: int, row_token: int, slot_row: int,
+                    workspace: int | None = None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_group_sort(ids, slots, topk, groups, offsets, row_token, slot_row, workspace or None,
+                                  workspace_bytes, stream), "gemm_group_sort")
+
+
+def gemm_group_combine(tokens: int, topk: int, N: int, type: int, src: int, src_rows: int, slot_row: int, out: int,
+                       weights: int | None = None, residual: int | None = None, stream: int = 0) -> None:
+    _check(load().gemm_group_combine(tokens, topk, N, type, src, src_rows, slot_row, weights or None,
+                                     residual or None, out, stream), "gemm_group_combine")
+
+
+def gemm_group_combine_grad(tokens: int, topk: int, N: int, type: int, d_out: int, src: int | None, src_rows: int,
+                            slot_row: int, weights: int | None, d_src: int, d_weights: int | None = None,
+                            stream: int = 0) -> None:
+    _check(load().gemm_group_combine_grad(tokens, topk, N, type, d_out, src or None, src_rows, slot_row,
+                                          weights or None, d_src, d_weights or None, stream),
+           "gemm_group_combine_grad")
+
+
+def gemm_act_grad_workspace_bytes(M: int, N: int, groups: int = 1) -> int:
+    return int(load().gemm_act_grad_workspace_bytes(M, N, groups))
+
+
+def gemm_act_grad(M: int, N: int, type: int, epilogue: int, d_c: int, z: int | None, d_z: int,
+                  d_bias: int | None = None, groups: int = 1, offsets: int | None = None,
+                  workspace: int | None = None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_act_grad(M, N, type, epilogue, d_c, z or None, d_z, d_bias or None, groups, offsets or None,
+                                workspace or None, workspace_bytes, stream), "gemm_act_grad")
+
+
 def gemm_plan_query(plan: int) -> dict:
     info = gemm_plan_info()
     _check(load().gemm_plan_query(plan, ctypes.byref(info)), "gemm_plan_query")
@@ -371,3 +478,45 @@ class Plan:
     def run_ws_noalloc(self, A: int, B: int, C: int, stream: int = 0, **epi) -> None:
         """gemm_run_ws_noalloc; keyword arguments as for the module-level gemm_run_ex."""
         gemm_run_ws_noalloc(self.handle, A, B, C, stream=stream, **epi)
+
+
+class GroupPlan:
+    """Owns one grouped-product plan; ``with GroupPlan(...) as p:`` destroys it
+    on exit.  ``tile_rows`` (0: the planner's choice) names the kernel family
+    as in gemm_group_plan_create_opt."""
+
+    def __init__(self, groups: int, M: int, N: int, K: int, dtype: int, layout: int, tile_rows: int = 0):
+        self.handle = 0                      # set before create, which may raise
+        if tile_rows == 0:
+            self.handle = gemm_group_plan_create(groups, M, N, K, dtype, layout)
+        else:
+            self.handle = gemm_group_plan_create_opt(groups, M, N, K, dtype, layout, tile_rows)
+
+    def close(self):
+        h, self.handle = self.handle, 0
+        # At interpreter exit the module's globals may already be cleared.
+        destroy = globals().get("gemm_group_plan_destroy")
+        if h and destroy is not None:
+            destroy(h)
+
+    __del__ = close
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def info(self) -> dict:
+        return gemm_group_plan_query(self.handle)
+
+    def preshuffled_b_bytes(self) -> int:
+        return gemm_group_preshuffled_b_bytes(self.handle)
+
+    def preshuffle_b(self, B: int, B_shuf: int, stream: int = 0) -> None:
+        gemm_group_preshuffle_b(self.handle, B, B_shuf, stream)
+
+    def run(self, A: int, B: int, C: int, offsets: int, row_index: int | None = None, a_rows: int = 0,
+            preact: int | None = None, stream: int = 0, **epi) -> None:
+        """gemm_group_run; epilogue keyword arguments as for the module-level gemm_run_ex."""
+        gemm_group_run(self.handle, A, B, C, offsets, row_index, a_rows, preact, stream=stream, **epi)

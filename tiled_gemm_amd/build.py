@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtgemm.so")
 SOURCES = ["capi.cpp", "gemm_tiled.hip", "gemm_pipe.hip", "gemm_dma.hip", "gemm_skinny.hip", "preshuffle.hip",
-           "splitk.hip", "gemm_mxw.hip"]
+           "splitk.hip", "gemm_mxw.hip", "capi_group.cpp", "group.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [
@@ -54,7 +54,7 @@ def build(extra_flags: list[str] | None = None, jobs: int | None = None) -> str:
     """Compile and link the library; returns its path."""
     extra = list(extra_flags or [])
     os.makedirs(BUILD, exist_ok=True)
-    jobs = jobs or min(len(SOURCES), max(1, (os.cpu_count() or 2) // 2))
+    jobs = jobs or min(len(SOURCES), max(1, os.cpu_count() or 2))
     with concurrent.futures.ThreadPoolExecutor(max_workers=jobs) as ex:
         objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
     tmp = LIB + ".tmp%d" % os.getpid()

@@ -11,8 +11,7 @@
 #include <new>
 #include <string>
 
-#include "tgemm.h"
-#include "kernels.hpp"
+#include "capi_util.hpp"
 #include "layout.hpp"
 
 using tg::Layout;
@@ -1105,3 +1104,27 @@ int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, 
 }
 
 }  // extern "C"
+
+// Shared with the other C entry points (capi_util.hpp).
+namespace tg {
+
+int capi_fail(int code, const char *fmt, ...)
+{
+    char buf[512];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    return fail(code, "%s", buf);
+}
+
+int capi_ok()
+{
+    ok();
+    return GEMM_OK;
+}
+
+int capi_check_device() { return check_device(); }
+int capi_epilogue(const gemm_epilogue_args *epi, EpiArgs *out) { return epi_from(epi, out); }
+
+}  // namespace tg

@@ -33,8 +33,7 @@
 //     lane 4 a + b of block q points at row k0 + a, columns c0 + 4 b .. + 3,
 //     and lane i of the block ends up with rows k0 .. k0 + 3 of column
 //     c0 + i.  Rows past K lie past the end of B and read as zeros.
-#include "device.hpp"
-#include "kernels.hpp"
+#include "group.hpp"
 
 namespace tg {
 
@@ -60,9 +59,10 @@ struct TiledCfg {
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
 };
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX>
-__global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p)
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false>
+__global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p0)
 {
+    TiledArgs p = p0;
     using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>;
     constexpr int FM = Cfg::FM, FN = Cfg::FN;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Cfg::LDS];
@@ -72,12 +72,19 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     const int wm = w / WGN, wn = w % WGN;
 
     int tm, tn;
-    tile_of_wg(blockIdx.x, p.grid, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    if constexpr (GRP) {
+        if (!group_enter<OUT>(p, BM, p.tiles_n, p.group_m, &tm, &tn))
+            return;
+    } else {
+        tile_of_wg(blockIdx.x, p.grid, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    }
     const int m0 = tm * BM, n0 = tn * BN;
     const int rows_a = min(p.M - m0, BM);
     const int rows_b = min(p.N - n0, BN);
     const uint32_t kb = (uint32_t)p.kbytes;
-    const auto rA = make_rsrc((const uint8_t *)p.A + (size_t)m0 * kb, (uint32_t)rows_a * kb);
+    const bool gather = GRP && p.grp.row_index;
+    const auto rA = gather ? make_rsrc(p.A, (uint32_t)p.grp.a_rows * kb)
+                           : make_rsrc((const uint8_t *)p.A + (size_t)m0 * kb, (uint32_t)rows_a * kb);
     // K x N B: the resource starts at column n0 and ends with the matrix, so
     // rows past K read zeros (columns past N read neighbouring data or zeros
     // and only feed columns of C that are never stored).
@@ -99,7 +106,8 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
         const int pc = (r * 4 + w) * 64 + l;
         const int row = pc >> 3;
         const int c = swz_chunk(row, pc & 7);
-        voffA[r] = (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
+        voffA[r] = gather ? group_a_off(p.grp, p.M, m0 + row, kb, (uint32_t)c * kChunkBytes)
+                          : (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
         tailA |= ((uint32_t)(c * kChunkBytes) < tail ? 1u : 0u) << r;
     }
     uint32_t voffB[Cfg::B_ROUNDS > 0 ? Cfg::B_ROUNDS : 1];
@@ -274,7 +282,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     // ---- epilogue: scale, bias, activation, convert, store.  Lane l holds
     // C[row][col .. col+3] with row = l % 16 and col = 4 * (l / 16) inside
     // each 16x16 tile.
-    const EpiView ev = epi_view(p.epi, p.M, p.N);
+    const EpiView ev = GRP ? group_epi_view(p.epi, p.grp, p.M, p.N) : epi_view(p.epi, p.M, p.N);
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
@@ -284,7 +292,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int row = wm * Cfg::WTM + i * 16 + r16;
-        const float sa = epi_row_scale(ev, m0 + row);
+        const float sa = GRP ? group_row_scale(ev, p.grp, p.M, m0 + row) : epi_row_scale(ev, m0 + row);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = n0 + wn * Cfg::WTN + j * 16 + 4 * q;
@@ -342,6 +350,31 @@ static const TiledVariant kTiled[] = {
     TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutBf16, true),
     TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutF32, true),
 };
+
+// Ragged row groups on 128 x 128 tiles, with the extended epilogue.
+template <int ELEM, bool BPRE, int OUT, bool BKN>
+static hipError_t launch_group_tiled(const TiledArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((gemm_tiled_kernel<128, 128, 2, 2, ELEM, BPRE, OUT, BKN, true, true>), dim3(a.grid),
+                       dim3(kTiledThreads), 0, s, a);
+    return hipGetLastError();
+}
+#define TG_GTILED(ELEM, BPRE, OUT, BKN)                                                    \
+    GroupVariant{128, 128, kTiledThreads, ELEM, OUT, BPRE, BKN, false,                      \
+                 TiledCfg<128, 128, 2, 2, ELEM, BPRE, OUT, BKN>::LDS, &launch_group_tiled<ELEM, BPRE, OUT, BKN>}
+
+static const GroupVariant kGroupTiled[] = {
+    TG_GTILED(kBf16, false, kOutBf16, false), TG_GTILED(kBf16, false, kOutF32, false),
+    TG_GTILED(kBf16, true, kOutBf16, false),  TG_GTILED(kBf16, true, kOutF32, false),
+    TG_GTILED(kFp8, false, kOutBf16, false),  TG_GTILED(kFp8, true, kOutBf16, false),
+    TG_GTILED(kBf16, false, kOutBf16, true),  TG_GTILED(kBf16, false, kOutF32, true),
+};
+
+const GroupVariant *group_tiled_variants(int *count)
+{
+    *count = (int)(sizeof(kGroupTiled) / sizeof(kGroupTiled[0]));
+    return kGroupTiled;
+}
 
 const TiledVariant *tiled_variants(int *count)
 {

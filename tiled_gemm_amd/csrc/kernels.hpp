@@ -29,6 +29,16 @@ struct EpiArgs {
     void *pre;              // launch_ex: nullptr or M x N of C's type
 };
 
+// Ragged row groups (the grouped kernels only; see group.hpp).
+struct GroupArgs {
+    const int32_t *offsets;     // groups + 1 row offsets, device data
+    const int32_t *row_index;   // nullptr, or the row of A behind every row of C
+    int32_t groups;
+    int32_t rows;               // rows the grouped operands have room for
+    int32_t a_rows;             // rows of A behind row_index
+    int64_t b_stride;           // bytes from one group's B to the next
+};
+
 struct TiledArgs {
     const void *A;
     const void *B;
@@ -55,6 +65,7 @@ struct TiledArgs {
     // with the identity epilogue.  splits == 1: the whole K, C as given.
     int32_t splits;
     int32_t split_steps;
+    GroupArgs grp;
 };
 
 // Sum of the split-K partials and the epilogue: C[m][n] = cvt(epi(sum over
@@ -106,6 +117,8 @@ struct SkinnyArgs {
     const uint8_t *sa_img;
     const uint8_t *sb_img;
     int32_t s_groups;
+    GroupArgs grp;
+    int32_t tiles_n;        // grouped kernels: 32-column tiles of C
 };
 
 struct PreshuffleArgs {
@@ -142,6 +155,58 @@ struct SkinnyVariant {
     bool preshuffled = false;   // B is the pre-shuffled image (register-staged B)
     hipError_t (*launch_ex)(const SkinnyArgs &, int grid, hipStream_t) = nullptr;   // extended epilogue
 };
+
+// A grouped kernel (group.hpp): tiles of bm rows, 0 < bm <= 64 the skinny ones.
+struct GroupVariant {
+    int bm, bn, threads;
+    int elem, out;
+    bool preshuffled, bkn, akm;
+    int lds_bytes;
+    hipError_t (*launch)(const TiledArgs &, hipStream_t);
+};
+const GroupVariant *group_dma_variants(int *count);
+const GroupVariant *group_tiled_variants(int *count);
+const GroupVariant *group_skinny_variants(int *count);
+
+constexpr int kMaxGroups = 1024;
+
+struct SortArgs {
+    const int32_t *ids;
+    int32_t *offsets, *row_token, *slot_row;
+    int32_t *counts;            // blocks x groups (workspace); unused with one block
+    int32_t slots, topk, groups;
+    int32_t blocks, block_slots;    // slots per block, a multiple of 1024
+    int32_t id_bits;            // bits that tell the ids 0 .. groups - 1 apart
+};
+hipError_t launch_group_sort(const SortArgs &, hipStream_t);
+
+struct CombineArgs {
+    const void *src;            // src_rows x N
+    const void *residual;       // combine: nullptr or tokens x N
+    const void *d_out;          // gradient: tokens x N
+    void *out;                  // combine: tokens x N; gradient: d_src, src_rows x N
+    const int32_t *slot_row;    // tokens x topk
+    const float *weights;       // nullptr (1) or tokens x topk
+    float *d_weights;           // gradient: nullptr or tokens x topk
+    int64_t tokens, N;
+    int32_t topk, src_rows;
+    int32_t type;               // kOutF32 or kOutBf16
+};
+hipError_t launch_group_combine(const CombineArgs &, hipStream_t);
+hipError_t launch_group_combine_grad(const CombineArgs &, hipStream_t);
+
+struct ActGradArgs {
+    const void *d_c, *z;
+    void *d_z;
+    float *d_bias;              // nullptr or groups x N
+    float *partial;             // max_chunks x N (workspace); nullptr without d_bias
+    const int32_t *offsets;     // nullptr: one group of M rows
+    int64_t N;
+    int32_t M, groups;
+    int32_t chunk, max_chunks;  // rows per chunk; an upper bound on the chunks of all groups
+    int32_t act, type;
+};
+hipError_t launch_act_grad(const ActGradArgs &, hipStream_t);
 
 constexpr int kSkinnyTileN = 32;
 constexpr int kTiledThreads = 256;
