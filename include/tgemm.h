@@ -459,10 +459,9 @@ typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after cre
 gemm_group_plan *gemm_group_plan_create(int groups, int64_t M, int64_t N, int64_t K, int dtype, int layout);
 
 /*
- * gemm_group_plan_create_opt -- the same with the kernel family named by the
- * rows of its tiles: 16, 32 or 64 (skinny kernels, GEMM_LAYOUT_BT and
- * GEMM_LAYOUT_BT_PRESHUFFLED), 128 (not GEMM_LAYOUT_AT_BN) or 256; 0 the
- * planner's own choice from M / groups.  Every choice computes the same C
+ * gemm_group_plan_create_opt -- the same with the kernel named by the rows of
+ * its tiles: 32, 64, 128 (not GEMM_LAYOUT_AT_BN) or 256; 0 the planner's own
+ * choice from M / groups.  Every choice computes the same C
  * within the same bound.  GEMM_ERR_UNSUPPORTED when the family has no kernel
  * for the dtype and layout.
  */
@@ -473,7 +472,6 @@ void gemm_group_plan_destroy(gemm_group_plan *plan);
 typedef struct {
     int64_t M, N, K;
     int32_t groups, dtype, layout;
-    int32_t kernel;          /* 0 tiled, 1 skinny                                     */
     int32_t tile_m, tile_n;
     int32_t threads, lds_bytes;
     int32_t grid;            /* workgroups of one launch (an upper bound on the tiles) */

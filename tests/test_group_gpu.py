@@ -119,7 +119,7 @@ def test_sort(tokens, topk, groups, lo, hi):
 
 # (type, layout, tile rows)
 FAMILIES = ([(t, lay, tile) for t in ("bf16", "f32", "e4m3") for lay in ("bt", "bt_preshuffled")
-             for tile in (16, 32, 64, 128, 256)] + [(t, "bn", tile) for t in ("bf16", "f32") for tile in (128, 256)])
+             for tile in (32, 64, 128, 256)] + [(t, "bn", tile) for t in ("bf16", "f32") for tile in (32, 64, 128, 256)])
 
 
 def grouped(plan, A, B, C, offsets, **kw):
@@ -177,7 +177,7 @@ def test_grouped_rows_bit_exact(types, layout, tile, groups, rows, gather):
     assert torch.equal(Z, dev(want_z, torch.float32).to(ct))
 
 
-@pytest.mark.parametrize("layout,tile", [("bt", 0), ("bt_preshuffled", 16), ("bt", 64), ("bt", 128), ("bt_preshuffled", 256),
+@pytest.mark.parametrize("layout,tile", [("bt", 0), ("bt_preshuffled", 32), ("bt", 64), ("bt", 128), ("bt_preshuffled", 256),
                                          ("bn", 128), ("bn", 256)])
 @pytest.mark.parametrize("kind", ["silu", "gelu", "none"])
 def test_grouped_rows_random(layout, tile, kind):
@@ -227,7 +227,7 @@ def test_weight_gradient_bit_exact(out, groups, rows, M, N):
 def test_offsets_outside_the_rows_are_clamped():
     rng = np.random.default_rng(2)
     a, b = ints(rng, (40, 64), -3, 3), ints(rng, (3, 32, 64), -3, 3)
-    for tile in (16, 128, 256):
+    for tile in (32, 128, 256):
         C = torch.full((40, 32), 5.0, dtype=torch.float32, device="cuda")
         with tg.GroupPlan(3, 40, 32, 64, F32O, tg.GEMM_LAYOUT_BT, tile_rows=tile) as p:
             grouped(p, dev(a, torch.bfloat16), dev(b, torch.bfloat16), C, i32([-7, 10, 2 ** 30, 2 ** 31 - 1]))

@@ -11,20 +11,20 @@ P = 1 << 40                     # an aligned address that is never read
 Q, R, S, T, U, V = (P + (i << 34) for i in range(1, 7))
 
 
-@pytest.mark.parametrize("groups,M,layout,tile", [(64, 64, PRE, 16), (64, 16 * 64, BT, 16), (8, 17 * 8, BT, 32),
-                                                  (8, 512, PRE, 64), (8, 520, BT, 128), (4, 4 * 192, BT, 128),
-                                                  (4, 4 * 193, BT, 256), (4, 1, BN, 128), (4, 4096, BN, 256)])
+@pytest.mark.parametrize("groups,M,layout,tile", [(64, 64, PRE, 32), (64, 24 * 64, BT, 32), (8, 25 * 8, BT, 64),
+                                                  (8, 56 * 8, PRE, 64), (8, 57 * 8, BT, 128), (4, 4 * 384, BT, 128),
+                                                  (4, 4 * 385, BT, 256), (4, 1, BN, 32), (4, 4096, BN, 256)])
 def test_tile_rule_and_grid(groups, M, layout, tile):
     with tg.GroupPlan(groups, M, 528, 256, BF, layout) as p:
         info = p.info()
-    assert info["tile_m"] == tile and info["kernel"] == (1 if tile <= 64 else 0)
+    assert info["tile_m"] == tile
     tiles_n = -(-528 // info["tile_n"])
     assert info["grid"] == min(M, (M + groups * (tile - 1)) // tile) * tiles_n
 
 
 def test_grid_bounds_every_split_of_the_rows():
     import itertools
-    for tile in (16, 128):
+    for tile in (32, 128):
         for M in (0, 1, 15, 16, 17, 40, 130):
             with tg.GroupPlan(3, M, 16, 64, BF, BT, tile_rows=tile) as p:
                 grid = p.info()["grid"]
@@ -52,8 +52,8 @@ def test_plan_refusals(args, why):
         tg.GroupPlan(*args)
 
 
-@pytest.mark.parametrize("layout,tile,why", [(BN, 16, "no grouped kernel"), (AT_BN, 128, "no grouped kernel"),
-                                             (BT, 48, "none of")])
+@pytest.mark.parametrize("layout,tile,why", [(AT_BN, 64, "no grouped kernel"), (AT_BN, 128, "no grouped kernel"),
+                                             (BT, 16, "none of")])
 def test_tile_choice_refusals(layout, tile, why):
     with pytest.raises(tg.GemmError, match=why):
         tg.GroupPlan(4, 64, 64, 64, BF, layout, tile_rows=tile)

@@ -97,8 +97,8 @@ class gemm_plan_info(ctypes.Structure):
 
 class gemm_group_plan_info(ctypes.Structure):
     _fields_ = [("M", ctypes.c_int64), ("N", ctypes.c_int64), ("K", ctypes.c_int64)] + [
-        (f, ctypes.c_int32) for f in ("groups", "dtype", "layout", "kernel", "tile_m", "tile_n", "threads",
-                                      "lds_bytes", "grid")]
+        (f, ctypes.c_int32) for f in ("groups", "dtype", "layout", "tile_m", "tile_n", "threads", "lds_bytes",
+                                      "grid")]
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}

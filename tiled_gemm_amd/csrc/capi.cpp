@@ -28,6 +28,10 @@ struct gemm_plan {
     // when splitting does not pay.
     const tg::TiledVariant *split_v;
     int32_t splits, split_steps, split_grid, split_tiles_m, split_tiles_n, split_group_m;
+    // The kernel behind gemm_run_res (kernel == 0): `tiled`, or smaller tiles
+    // where those would leave CUs idle.  nullptr: no extended epilogue.
+    const tg::TiledVariant *ex_v;
+    int32_t ex_grid, ex_tiles_m, ex_tiles_n, ex_group_m;
 };
 
 namespace {
@@ -311,6 +315,38 @@ void plan_split(gemm_plan *p, int kc, int forced)
     p->split_grid = (int32_t)(tiles * s);
 }
 
+// The tiled kernel of the extended epilogue.
+void plan_ex(gemm_plan *p, int kc)
+{
+    const gemm_plan_info &I = p->info;
+    p->ex_v = p->tiled && p->tiled->launch_ex ? p->tiled : nullptr;
+    if (kc == GEMM_KERNEL_AUTO && p->ex_v && I.tile_m == 128) {
+        // A workgroup that is alone on its CU waits for memory at every step, so
+        // up to one tile per CU the tiles come from a kernel with more steps in
+        // flight, and are as small as still gives every CU at most one (the
+        // list runs from small to large).  Measured, 128 x 128 with two stages
+        // against the choice: 333 x 4096 x 4160 e4m3 43 -> 25 us (64 x 128),
+        // 100 x 4096 x 4096 bf16 65 -> 23 us (64 x 64), 2000 x 2048 x 2048 bf16
+        // 38 -> 32 us (128 x 128).
+        int n = 0;
+        const tg::TiledVariant *v = tg::small_variants(&n);
+        const tg::TiledVariant *s = first_of(v, n, [&](const tg::TiledVariant &x) {
+            return x.elem == p->tiled->elem && x.out == p->tiled->out && x.preshuffled == p->tiled->preshuffled &&
+                   x.bkn == p->tiled->bkn && ((I.M + x.bm - 1) / x.bm) * ((I.N + x.bn - 1) / x.bn) <= 256;
+        });
+        if (s)
+            p->ex_v = s;
+    }
+    if (!p->ex_v)
+        return;
+    p->ex_tiles_m = (int32_t)((I.M + p->ex_v->bm - 1) / p->ex_v->bm);
+    p->ex_tiles_n = (int32_t)((I.N + p->ex_v->bn - 1) / p->ex_v->bn);
+    p->ex_grid = p->ex_tiles_m * p->ex_tiles_n;
+    p->ex_group_m = p->ex_v->bm >= 256 ? 4 : 8;
+    if (p->ex_group_m > p->ex_tiles_m)
+        p->ex_group_m = p->ex_tiles_m > 0 ? p->ex_tiles_m : 1;
+}
+
 Layout make(std::initializer_list<int64_t> shape, std::initializer_list<int64_t> stride)
 {
     Layout L{};
@@ -555,6 +591,7 @@ gemm_plan *gemm_plan_create_opt(int64_t M, int64_t N, int64_t K, int dtype, int 
         return nullptr;
     }
     plan_split(p, kc, forced_splits);
+    plan_ex(p, kc);
     I.ws_splits = p->splits;
     I.ws_grid = p->splits > 1 ? p->split_grid : I.grid;
     I.scale_form = wide_scales(p) ? 1 : 0;
@@ -762,14 +799,14 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         a.lda_bytes = (int32_t)(I.M * I.elem_bytes);
         a.k_tiles = plan->k_tiles;
         a.tail_bytes = plan->tail_bytes;
-        a.grid = I.grid;
-        a.tiles_m = I.tiles_m;
-        a.tiles_n = I.tiles_n;
-        a.group_m = I.group_m;
+        a.grid = ex ? plan->ex_grid : I.grid;
+        a.tiles_m = ex ? plan->ex_tiles_m : I.tiles_m;
+        a.tiles_n = ex ? plan->ex_tiles_n : I.tiles_n;
+        a.group_m = ex ? plan->ex_group_m : I.group_m;
         a.sa_img = (const uint8_t *)sa_img;
         a.sb_img = (const uint8_t *)sb_img;
         a.s_groups = (int32_t)scale_groups(I.K);
-        e = (ex ? plan->tiled->launch_ex : plan->tiled->launch)(a, stream);
+        e = ex ? plan->ex_v->launch_ex(a, stream) : plan->tiled->launch(a, stream);
     }
     if (e != hipSuccess)
         return fail(GEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
@@ -903,7 +940,7 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
                    overlap(preact, cbytes, B, (size_t)I.N * plan->kbytes_b)))
         return fail(GEMM_ERR_INVALID_ARG, "preact overlaps A, B, C or the residual");
     if ((residual || preact) &&
-        (I.kernel == 1 ? plan->skinny->launch_ex == nullptr : plan->tiled->launch_ex == nullptr))
+        (I.kernel == 1 ? plan->skinny->launch_ex == nullptr : plan->ex_v == nullptr))
         return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no residual epilogue (GEMM_KERNEL_AUTO and "
                                           "GEMM_KERNEL_TILE256 have)");
     e->res = residual;

@@ -40,22 +40,22 @@ const tg::GroupVariant *find(const tg::GroupVariant *v, int n, int bm, int elem,
 const tg::GroupVariant *pick(int bm, int elem, int out, int layout)
 {
     int n = 0;
-    const tg::GroupVariant *v = bm == 256   ? tg::group_dma_variants(&n)
-                                : bm == 128 ? tg::group_tiled_variants(&n)
-                                            : tg::group_skinny_variants(&n);
+    const tg::GroupVariant *v = bm == 256 ? tg::group_dma_variants(&n) : tg::group_tiled_variants(&n);
     return find(v, n, bm, elem, out, layout);
 }
 
-// Rows per tile from the mean rows per group: the smallest tile that holds
-// the mean, the skinny kernels up to 64 rows (the layouts that have them).
+// Rows per tile from the mean rows per group, M being the rows there is room
+// for.  Up to 24 rows (decode) the 32-row tiles stream the active experts'
+// weights at the rate of a copy; larger tiles read the same weights with fewer
+// workgroups in flight.  Measured (bf16, 64 groups, N 2048, K 1024, us for
+// tiles of 32 / 64 / 128 / 256): mean 1: 32 / 38 / 48 / 91; mean 32: 58 / 55 /
+// 63 / 99; mean 64: 77 / 70 / 64 / 99; mean 200: 173 / 131 / 127 / 145.
 int default_tile(int groups, int64_t M, int layout)
 {
     if (layout == GEMM_LAYOUT_AT_BN)
         return 256;
     const int64_t mean = (M + groups - 1) / groups;
-    if (layout != GEMM_LAYOUT_BN && mean <= 64)
-        return mean <= 16 ? 16 : (mean <= 32 ? 32 : 64);
-    return mean <= 192 ? 128 : 256;
+    return mean <= 24 ? 32 : (mean <= 56 ? 64 : (mean <= 384 ? 128 : 256));
 }
 
 }  // namespace
@@ -69,9 +69,8 @@ gemm_group_plan *gemm_group_plan_create_opt(int groups, int64_t M, int64_t N, in
         capi_fail(GEMM_ERR_INVALID_ARG, "groups=%d outside 1..%d", groups, GEMM_GROUP_MAX);
         return nullptr;
     }
-    if (tile_rows != 0 && tile_rows != 16 && tile_rows != 32 && tile_rows != 64 && tile_rows != 128 &&
-        tile_rows != 256) {
-        capi_fail(GEMM_ERR_INVALID_ARG, "tile_rows=%d is none of 0, 16, 32, 64, 128, 256", tile_rows);
+    if (tile_rows != 0 && tile_rows != 32 && tile_rows != 64 && tile_rows != 128 && tile_rows != 256) {
+        capi_fail(GEMM_ERR_INVALID_ARG, "tile_rows=%d is none of 0, 32, 64, 128, 256", tile_rows);
         return nullptr;
     }
     if (dtype != GEMM_BF16_OUT_F32 && dtype != GEMM_BF16_OUT_BF16 && dtype != GEMM_E4M3_OUT_BF16) {
@@ -131,7 +130,6 @@ gemm_group_plan *gemm_group_plan_create_opt(int groups, int64_t M, int64_t N, in
     I.groups = groups;
     I.dtype = dtype;
     I.layout = layout;
-    I.kernel = bm <= 64 ? 1 : 0;
     I.tile_m = bm;
     I.tile_n = p->v->bn;
     I.threads = p->v->threads;

@@ -26,35 +26,10 @@
 //
 // The partial tiles of the waves are summed through LDS in a fixed wave order
 // (deterministic), then scaled, converted and stored.
-#include "group.hpp"
+#include "device.hpp"
+#include "kernels.hpp"
 
 namespace tg {
-
-// Grouped: restricts the arguments to this workgroup's rows, at most 16 MB of
-// one group, and gives its column tile.  Tiles of one group walk the rows
-// first, so a group with more rows re-reads its B columns from the L2.
-template <int MB, int OUT>
-__device__ inline bool skinny_enter(SkinnyArgs &p, int *wg)
-{
-    int tm, tn;
-    if (!group_enter<OUT>(p, MB * 16, p.tiles_n, 1 << 14, &tm, &tn))
-        return false;
-    const int r0 = tm * MB * 16;
-    const size_t c_off = (size_t)r0 * (size_t)p.N * (OUT == kOutF32 ? 4u : 2u);
-    if (p.grp.row_index) {
-        p.grp.row_index += r0;
-    } else {
-        p.A = (const uint8_t *)p.A + (size_t)r0 * (size_t)p.kbytes;
-        if (p.epi.sa && p.epi.sa_rows)
-            p.epi.sa += r0;
-    }
-    p.C = (uint8_t *)p.C + c_off;
-    if (p.epi.pre)
-        p.epi.pre = (uint8_t *)p.epi.pre + c_off;
-    p.M = min(p.M - r0, MB * 16);
-    *wg = tn;
-    return true;
-}
 
 constexpr int kRedPitch = kSkinnyTileN + 1;   // padded reduction row (bank spread)
 
@@ -64,7 +39,7 @@ constexpr int kRedPitch = kSkinnyTileN + 1;   // padded reduction row (bank spre
 // IUNIT = 0: fp32 accumulators.  Otherwise the accumulators hold int32 sums
 // (integer MFMAs): the waves' partials are summed in int32 (exact), then
 // converted to fp32 and multiplied by 1 / IUNIT (a power of two, exact).
-template <int MB, int OUT, int WAVES, int IUNIT = 0, bool EX = false, bool GRP = false>
+template <int MB, int OUT, int WAVES, int IUNIT = 0, bool EX = false>
 __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB][kSkinnyTileN / 16], uint8_t *lds,
                                      int n0)
 {
@@ -84,7 +59,7 @@ __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB]
                 red[w][i * 16 + r16][j * 16 + 4 * q + v] = acc[i][j][v];
     __syncthreads();
 
-    const EpiView ev = GRP ? group_epi_view(p.epi, p.grp, p.M, p.N) : epi_view(p.epi, p.M, p.N);
+    const EpiView ev = epi_view(p.epi, p.M, p.N);
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc(p.C, (uint32_t)p.M * ldc);
@@ -112,7 +87,7 @@ __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB]
         const int n = n0 + col;
         float sb[2], bz[2];
         epi_col2(ev, n, sb, bz);
-        const float sa = GRP ? group_row_scale(ev, p.grp, p.M, row) : epi_row_scale(ev, row);
+        const float sa = epi_row_scale(ev, row);
         const uint32_t voffc = (row < p.M && n < p.N) ? (uint32_t)row * ldc + (uint32_t)n * OB : kOobOffset;
         if constexpr (EX)
             epi_finish2<OUT>(ev, ex, s0, s1, sa, sb, bz, voffc);
@@ -143,15 +118,9 @@ struct SkinnyCfg {
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX, bool GRP = false>
-__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const SkinnyArgs p0)
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX>
+__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const SkinnyArgs p)
 {
-    SkinnyArgs p = p0;
-    int wg = blockIdx.x;
-    if constexpr (GRP) {
-        if (!skinny_enter<MB, OUT>(p, &wg))
-            return;
-    }
     using Cfg = SkinnyCfg<MB, WAVES, DEPTH>;
     constexpr int NB = kSkinnyTileN / 16;
     constexpr int L = Cfg::LOADS;
@@ -160,10 +129,10 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const Skinny
     const int w = wave_id();
     const int l = lane_id();
     const int q = l >> 4, r16 = l & 15;
-    const int n0 = wg * kSkinnyTileN;
+    const int n0 = blockIdx.x * kSkinnyTileN;
     const uint32_t kb = (uint32_t)p.kbytes;
     const int rows_b = min(p.N - n0, kSkinnyTileN);
-    const auto rA = make_rsrc(p.A, (uint32_t)(GRP && p.grp.row_index ? p.grp.a_rows : p.M) * kb);
+    const auto rA = make_rsrc(p.A, (uint32_t)p.M * kb);
     const auto rB = make_rsrc((const uint8_t *)p.B + (size_t)n0 * kb, (uint32_t)rows_b * kb);
     const int nk = p.k_tiles;
     const uint32_t tail = (uint32_t)p.tail_bytes;
@@ -179,17 +148,14 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const Skinny
         const int row = 8 * j + (l >> 3);
         const int c = swz_chunk(row, l & 7);
         const int src_row = row < Cfg::ROWS_A ? row : row - Cfg::ROWS_A;
-        if (GRP && row < Cfg::ROWS_A)
-            voff[j] = group_a_off(p.grp, p.M, row, kb, (uint32_t)c * kChunkBytes);
-        else
-            voff[j] = (uint32_t)src_row * kb + (uint32_t)c * kChunkBytes;
+        voff[j] = (uint32_t)src_row * kb + (uint32_t)c * kChunkBytes;
         half_keep |= (c < kChunksPerRow / 2 ? 1u : 0u) << j;
     }
 
     const int per = (nk + WAVES - 1) / WAVES;
     const int first = w * per;
     const int nt = max(0, min(per, nk - first));         // this wave's steps
-    const int rot = ROTATE ? (int)(((uint32_t)wg * 37u) % (uint32_t)max(nk, 1)) : 0;
+    const int rot = ROTATE ? (int)((blockIdx.x * 37u) % (uint32_t)max(nk, 1)) : 0;
 
     // Step t of this wave into ring stage s (every load is issued; the ones
     // past the run or past K in a half-filled last step are out of range).
@@ -269,7 +235,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const Skinny
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);
     __syncthreads();
 
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : 0, EX, GRP>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : 0, EX>(p, acc, lds, n0);
 }
 
 template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX = false>
@@ -305,15 +271,9 @@ struct SkinnyPreCfg {
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX, bool GRP = false>
-__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const SkinnyArgs p0)
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX>
+__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const SkinnyArgs p)
 {
-    SkinnyArgs p = p0;
-    int wg = blockIdx.x;
-    if constexpr (GRP) {
-        if (!skinny_enter<MB, OUT>(p, &wg))
-            return;
-    }
     // Packed int4 B (W4A8): one 1 KiB block per 16 columns and step, i.e. the
     // 64 B-bytes of 128 K values per row; lane group q holds values 32 q ..
     // 32 q + 31, unpacked into two int8 operands, half h pairing with A
@@ -344,11 +304,11 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     const int w = wave_id();
     const int l = lane_id();
     const int q = l >> 4, r16 = l & 15;
-    const int n0 = wg * kSkinnyTileN;
+    const int n0 = blockIdx.x * kSkinnyTileN;
     const uint32_t kb = (uint32_t)p.kbytes;
     const int rows_b = min(p.N - n0, kSkinnyTileN);
     const uint32_t kbB = (uint32_t)p.kbytes_b;
-    const auto rA = make_rsrc(p.A, (uint32_t)(GRP && p.grp.row_index ? p.grp.a_rows : p.M) * kb);
+    const auto rA = make_rsrc(p.A, (uint32_t)p.M * kb);
     // The workgroup's 16-column blocks are contiguous in the image (16 * kbB
     // bytes each); a block past N lies past the record count (zeros).
     const auto rB = make_rsrc((const uint8_t *)p.B + (size_t)n0 * kbB, (uint32_t)rows_b * kbB);
@@ -363,8 +323,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     for (int j = 0; j < AL; ++j) {
         const int row = 8 * j + (l >> 3);
         const int c = swz_chunk(row, l & 7);
-        voffA[j] = GRP ? group_a_off(p.grp, p.M, row, kb, (uint32_t)c * kChunkBytes)
-                       : (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
+        voffA[j] = (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
         half_keep |= (c < kChunksPerRow / 2 ? 1u : 0u) << j;
     }
 
@@ -374,7 +333,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     const int per = MX ? ((nk + WAVES - 1) / WAVES + SPG - 1) / SPG * SPG : (nk + WAVES - 1) / WAVES;
     const int first = INTER ? w : w * per;
     const int nt = INTER ? (w < nk ? (nk - w + WAVES - 1) / WAVES : 0) : max(0, min(per, nk - first));
-    const int rot = (ORD == 0 || ORD == 2) ? (int)(((uint32_t)wg * 37u) % (uint32_t)max(nk, 1)) : 0;
+    const int rot = (ORD == 0 || ORD == 2) ? (int)((blockIdx.x * 37u) % (uint32_t)max(nk, 1)) : 0;
 
     // B of one step: image blocks BH kt + h of 16-column block j.
     u32x4 bq[DEPTH][NB][BH];
@@ -511,7 +470,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     if constexpr (MX)
         mfma_drain_acc(acc);                      // the scaled MFMAs are inline assembly
     __syncthreads();
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : (W4 ? 16 : 0), EX, GRP>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : (W4 ? 16 : 0), EX>(p, acc, lds, n0);
 }
 
 template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX = false>
@@ -573,56 +532,6 @@ static const SkinnyVariant kSkinny[] = {
     TG_SKINNY_PRE(4, kBf16, kOutBf16, 4, 4),                                                    // 44
 #endif
 };
-
-// Ragged row groups, with the extended epilogue.
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BPRE>
-static hipError_t launch_group_skinny(const TiledArgs &t, hipStream_t s)
-{
-    SkinnyArgs a{};
-    a.A = t.A;
-    a.B = t.B;
-    a.C = t.C;
-    a.epi = t.epi;
-    a.M = t.M;
-    a.N = t.N;
-    a.kbytes = t.kbytes;
-    a.k_tiles = t.k_tiles;
-    a.tail_bytes = t.tail_bytes;
-    a.kbytes_b = t.kbytes_b;
-    a.grp = t.grp;
-    a.tiles_n = t.tiles_n;
-    if constexpr (BPRE)
-        hipLaunchKernelGGL((gemm_skinny_pre_kernel<MB, ELEM, OUT, WAVES, DEPTH, false, 1, true, true>), dim3(t.grid),
-                           dim3(64 * WAVES), 0, s, a);
-    else
-        hipLaunchKernelGGL((gemm_skinny_kernel<MB, ELEM, OUT, WAVES, DEPTH, true, true, true>), dim3(t.grid),
-                           dim3(64 * WAVES), 0, s, a);
-    return hipGetLastError();
-}
-#define TG_GSKINNY(MB, ELEM, OUT, WAVES, DEPTH)                                                              \
-    GroupVariant{MB * 16, kSkinnyTileN, 64 * WAVES, ELEM, OUT, false, false, false,                           \
-                 SkinnyCfg<MB, WAVES, DEPTH>::LDS, &launch_group_skinny<MB, ELEM, OUT, WAVES, DEPTH, false>}
-#define TG_GSKINNY_PRE(MB, ELEM, OUT, WAVES, DEPTH)                                                          \
-    GroupVariant{MB * 16, kSkinnyTileN, 64 * WAVES, ELEM, OUT, true, false, false,                            \
-                 SkinnyPreCfg<MB, WAVES, DEPTH, false, 2>::LDS,                                               \
-                 &launch_group_skinny<MB, ELEM, OUT, WAVES, DEPTH, true>}
-
-static const GroupVariant kGroupSkinny[] = {
-    TG_GSKINNY(1, kBf16, kOutBf16, 8, 3), TG_GSKINNY(2, kBf16, kOutBf16, 8, 2), TG_GSKINNY(4, kBf16, kOutBf16, 4, 3),
-    TG_GSKINNY(1, kBf16, kOutF32, 8, 3), TG_GSKINNY(2, kBf16, kOutF32, 8, 2), TG_GSKINNY(4, kBf16, kOutF32, 4, 3),
-    TG_GSKINNY(1, kFp8, kOutBf16, 8, 3), TG_GSKINNY(2, kFp8, kOutBf16, 8, 2), TG_GSKINNY(4, kFp8, kOutBf16, 4, 3),
-    TG_GSKINNY_PRE(1, kBf16, kOutBf16, 12, 2), TG_GSKINNY_PRE(2, kBf16, kOutBf16, 12, 2),
-    TG_GSKINNY_PRE(4, kBf16, kOutBf16, 8, 2), TG_GSKINNY_PRE(1, kBf16, kOutF32, 12, 2),
-    TG_GSKINNY_PRE(2, kBf16, kOutF32, 12, 2), TG_GSKINNY_PRE(4, kBf16, kOutF32, 8, 2),
-    TG_GSKINNY_PRE(1, kFp8, kOutBf16, 12, 2), TG_GSKINNY_PRE(2, kFp8, kOutBf16, 12, 2),
-    TG_GSKINNY_PRE(4, kFp8, kOutBf16, 8, 2),
-};
-
-const GroupVariant *group_skinny_variants(int *count)
-{
-    *count = (int)(sizeof(kGroupSkinny) / sizeof(kGroupSkinny[0]));
-    return kGroupSkinny;
-}
 
 const SkinnyVariant *skinny_variants(int *count)
 {

@@ -37,7 +37,10 @@
 
 namespace tg {
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN = false>
+// NS > 2: a ring of NS LDS stages with NS - 1 steps in flight, for grids that
+// leave most CUs one workgroup or none, where a step waits for memory and no
+// neighbour hides it.  A pre-shuffled B then goes through LDS as well.
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN = false, int NS = 2>
 struct TiledCfg {
     static constexpr int kWaves = 4;
     static_assert(WGM * WGN == kWaves, "4 waves per workgroup");
@@ -46,12 +49,13 @@ struct TiledCfg {
     static constexpr int FM = WTM / 16;              // 16x16 MFMA tiles per wave (rows)
     static constexpr int FN = WTN / 16;              // (columns)
     static constexpr int A_BYTES = BM * kTileKBytes;
-    static constexpr int B_BYTES = BPRE ? 0 : BN * kTileKBytes;   // N x K: BN rows; K x N: 64 k-rows of BN * 2
+    static constexpr bool BREG = BPRE && NS == 2;                   // pre-shuffled B straight to registers
+    static constexpr int B_BYTES = BREG ? 0 : BN * kTileKBytes;   // N x K: BN rows; K x N: 64 k-rows of BN * 2
     static constexpr int KN_ROW = BN * 2;                          // bytes of one K-row of a K x N tile (bf16)
     static constexpr int KN_CPR = KN_ROW / kChunkBytes;            // its 16-byte chunks
     static_assert(!BKN || (ELEM == kBf16 && !BPRE && KN_CPR >= 16), "K x N B: bf16, staged in LDS");
     static constexpr int STAGE = A_BYTES + B_BYTES;
-    static constexpr int LDS = 2 * STAGE;
+    static constexpr int LDS = NS * STAGE;
     static constexpr int ROUND_BYTES = kTiledThreads * kChunkBytes;   // one 16B load per thread
     static constexpr int A_ROUNDS = A_BYTES / ROUND_BYTES;
     static constexpr int B_ROUNDS = B_BYTES / ROUND_BYTES;
@@ -59,11 +63,12 @@ struct TiledCfg {
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
 };
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false>
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false, int NS = 2>
 __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p0)
 {
     TiledArgs p = p0;
-    using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>;
+    using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, NS>;
+    constexpr bool BREG = Cfg::BREG;
     constexpr int FM = Cfg::FM, FN = Cfg::FN;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Cfg::LDS];
 
@@ -121,6 +126,11 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
             const int c = (pc % Cfg::KN_CPR) ^ bkn_swz(row);
             voffB[r] = (uint32_t)row * ldb + (uint32_t)c * kChunkBytes;
             tailB |= 1u << r;
+        } else if constexpr (BPRE) {
+            // operand block u: column block u / 2, K half u % 2, 1 KiB of the image
+            const int u = r * 4 + w;
+            voffB[r] = (uint32_t)(u >> 1) * 16u * kb + (uint32_t)(u & 1) * 1024u + (uint32_t)l * 16u;
+            tailB |= ((uint32_t)((u & 1) * 64) < tail ? 1u : 0u) << r;
         } else {
             const int row = pc >> 3;
             const int c = swz_chunk(row, pc & 7);
@@ -132,19 +142,22 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     auto issue_lds = [&](int kt, int stage) {
         const bool part = (kt == nk - 1) && tail != (uint32_t)kTileKBytes;
         uint8_t *sA = lds + stage * Cfg::STAGE;
+        // with a ring, steps past the last one load zeros, so that every step
+        // has the same number of loads in flight
+        const bool in = NS == 2 || kt < nk;
         const uint32_t soff = (uint32_t)kt * kTileKBytes;
 #pragma unroll
         for (int r = 0; r < Cfg::A_ROUNDS; ++r) {
-            const uint32_t vo = (!part || ((tailA >> r) & 1u)) ? voffA[r] : kOobOffset;
+            const uint32_t vo = in && (!part || ((tailA >> r) & 1u)) ? voffA[r] : kOobOffset;
             buf_load16_to_lds(rA, sA + (r * 4 + w) * 1024, vo, soff);
         }
-        if constexpr (!BPRE) {
+        if constexpr (!BREG) {
             uint8_t *sB = sA + Cfg::A_BYTES;
-            // K x N: a step is 64 K-rows of B
-            const uint32_t soffB = BKN ? (uint32_t)kt * 64u * ldb : soff;
+            // K x N: a step is 64 K-rows of B; pre-shuffled: two 1 KiB blocks
+            const uint32_t soffB = !in ? 0u : (BKN ? (uint32_t)kt * 64u * ldb : (BPRE ? (uint32_t)kt * 2048u : soff));
 #pragma unroll
             for (int r = 0; r < Cfg::B_ROUNDS; ++r) {
-                const uint32_t vo = (!part || ((tailB >> r) & 1u)) ? voffB[r] : kOobOffset;
+                const uint32_t vo = in && (!part || ((tailB >> r) & 1u)) ? voffB[r] : kOobOffset;
                 buf_load16_to_lds(rB, sB + (r * 4 + w) * 1024, vo, soffB);
             }
         }
@@ -207,8 +220,10 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
                 u32x4 bf[FN];
 #pragma unroll
                 for (int j = 0; j < FN; ++j) {
-                    if constexpr (BPRE)
+                    if constexpr (BREG)
                         bf[j] = bq[j][s];
+                    else if constexpr (BPRE)
+                        bf[j] = lds_load16(sB + ((wn * FN + j) * 2 + s) * 1024 + l * 16);
                     else if constexpr (BKN)
                         bf[j] = bkn_frag(sB, s, j);
                     else
@@ -226,9 +241,12 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
             u32x4 blo[FN], bhi[FN];
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
-                if constexpr (BPRE) {
+                if constexpr (BREG) {
                     blo[j] = bq[j][0];
                     bhi[j] = bq[j][1];
+                } else if constexpr (BPRE) {
+                    blo[j] = lds_load16(sB + (wn * FN + j) * 2048 + l * 16);
+                    bhi[j] = lds_load16(sB + (wn * FN + j) * 2048 + 1024 + l * 16);
                 } else {
                     const int row = wn * Cfg::WTN + j * 16 + r16;
                     blo[j] = lds_load16(lds_chunk(sB, row, q));
@@ -258,19 +276,45 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
         __syncthreads();
         if (kt + 1 < nk) {
             issue_lds(kt + 1, stage ^ 1);
-            if constexpr (BPRE)
+            if constexpr (BREG)
                 load_bpre(kt + 1, nxt);
         }
         compute(stage, cur);
     };
-    if (nk > 0) {
+    if constexpr (NS > 2) {
+        // NS - 1 steps in flight: before a step, all but the youngest NS - 2
+        // have landed (vmcnt) for every wave (the barrier), and every wave has
+        // read the stage that the step's own loads then refill.  (Reading the
+        // next step's fragments beside the MFMAs, and rings of 6 and 8 stages,
+        // measured the same: the steps are bound by the loads' rate, not
+        // their latency.)
+        constexpr int kVm = (NS - 2) * (Cfg::A_ROUNDS + Cfg::B_ROUNDS);
+        static_assert(kVm < 64, "vmcnt holds 6 bits");
+        constexpr int kWaitOldest = (kWaitVmcnt0 & ~0xC00F) | (kVm & 0xF) | ((kVm >> 4) << 14);
+        constexpr int kWaitLds = 0xC07F;                 // lgkmcnt(0) only
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s)
+            issue_lds(s, s);
+        int s = 0;
+        for (int kt = 0; kt < nk; ++kt) {
+            __builtin_amdgcn_s_waitcnt(kWaitOldest & kWaitLds);
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_barrier();
+            __builtin_amdgcn_sched_barrier(0);
+            issue_lds(kt + NS - 1, s == 0 ? NS - 1 : s - 1);
+            issue_fence();
+            compute(s, bq0);
+            s = s + 1 == NS ? 0 : s + 1;
+        }
+        __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);         // no load may outlive the workgroup's LDS
+    } else if (nk > 0) {
         issue_lds(0, 0);
-        if constexpr (BPRE)
+        if constexpr (BREG)
             load_bpre(0, bq0);
     }
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = 0; NS == 2 && kt < nk; ++kt) {
         step(kt, kt & 1, bq0, bq1);
-        if constexpr (BPRE) {
+        if constexpr (BREG) {
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 bq0[j][0] = bq1[j][0];
@@ -351,29 +395,65 @@ static const TiledVariant kTiled[] = {
     TG_TILED_X(128, 128, 2, 2, kBf16, false, kOutF32, true),
 };
 
-// Ragged row groups on 128 x 128 tiles, with the extended epilogue.
-template <int ELEM, bool BPRE, int OUT, bool BKN>
+// Ragged row groups, with the extended epilogue.
+template <int BM, int BN, int WGM, int NS, int ELEM, bool BPRE, int OUT, bool BKN>
 static hipError_t launch_group_tiled(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_tiled_kernel<128, 128, 2, 2, ELEM, BPRE, OUT, BKN, true, true>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, WGM, 4 / WGM, ELEM, BPRE, OUT, BKN, true, true, NS>), dim3(a.grid),
                        dim3(kTiledThreads), 0, s, a);
     return hipGetLastError();
 }
-#define TG_GTILED(ELEM, BPRE, OUT, BKN)                                                    \
-    GroupVariant{128, 128, kTiledThreads, ELEM, OUT, BPRE, BKN, false,                      \
-                 TiledCfg<128, 128, 2, 2, ELEM, BPRE, OUT, BKN>::LDS, &launch_group_tiled<ELEM, BPRE, OUT, BKN>}
+#define TG_GTILED(BM, BN, WGM, NS, ELEM, BPRE, OUT, BKN)                                   \
+    GroupVariant{BM, BN, kTiledThreads, ELEM, OUT, BPRE, BKN, false,                        \
+                 TiledCfg<BM, BN, WGM, 4 / WGM, ELEM, BPRE, OUT, BKN, NS>::LDS,             \
+                 &launch_group_tiled<BM, BN, WGM, NS, ELEM, BPRE, OUT, BKN>}
+#define TG_GTILED_ALL(...)                                                                 \
+    TG_GTILED(__VA_ARGS__, kBf16, false, kOutBf16, false), TG_GTILED(__VA_ARGS__, kBf16, false, kOutF32, false), \
+    TG_GTILED(__VA_ARGS__, kBf16, true, kOutBf16, false),  TG_GTILED(__VA_ARGS__, kBf16, true, kOutF32, false),  \
+    TG_GTILED(__VA_ARGS__, kFp8, false, kOutBf16, false),  TG_GTILED(__VA_ARGS__, kFp8, true, kOutBf16, false),  \
+    TG_GTILED(__VA_ARGS__, kBf16, false, kOutBf16, true),  TG_GTILED(__VA_ARGS__, kBf16, false, kOutF32, true)
 
 static const GroupVariant kGroupTiled[] = {
-    TG_GTILED(kBf16, false, kOutBf16, false), TG_GTILED(kBf16, false, kOutF32, false),
-    TG_GTILED(kBf16, true, kOutBf16, false),  TG_GTILED(kBf16, true, kOutF32, false),
-    TG_GTILED(kFp8, false, kOutBf16, false),  TG_GTILED(kFp8, true, kOutBf16, false),
-    TG_GTILED(kBf16, false, kOutBf16, true),  TG_GTILED(kBf16, false, kOutF32, true),
+    TG_GTILED_ALL(32, 128, 1, 4),
+    TG_GTILED_ALL(64, 128, 2, 3),
+    TG_GTILED_ALL(128, 128, 2, 2),
 };
 
 const GroupVariant *group_tiled_variants(int *count)
 {
     *count = (int)(sizeof(kGroupTiled) / sizeof(kGroupTiled[0]));
     return kGroupTiled;
+}
+
+// The extended epilogue on smaller tiles with a ring of stages, for grids
+// that leave CUs idle (plan_ex in capi.cpp), small tiles first.
+template <int BM, int BN, int NS, int ELEM, bool BPRE, int OUT, bool BKN>
+static hipError_t launch_small(const TiledArgs &a, hipStream_t s)
+{
+    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, true, false, NS>), dim3(a.grid),
+                       dim3(kTiledThreads), 0, s, a);
+    return hipGetLastError();
+}
+#define TG_SMALL(BM, BN, NS, ELEM, BPRE, OUT, BKN)                                         \
+    TiledVariant{BM, BN, 2, 2, ELEM, OUT, BPRE, TiledCfg<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, NS>::LDS, NS, \
+                 nullptr, BKN, false, &launch_small<BM, BN, NS, ELEM, BPRE, OUT, BKN>}
+#define TG_SMALL_ALL(BM, BN, NS)                                                           \
+    TG_SMALL(BM, BN, NS, kBf16, false, kOutBf16, false), TG_SMALL(BM, BN, NS, kBf16, false, kOutF32, false), \
+    TG_SMALL(BM, BN, NS, kBf16, true, kOutBf16, false),  TG_SMALL(BM, BN, NS, kBf16, true, kOutF32, false),  \
+    TG_SMALL(BM, BN, NS, kFp8, false, kOutBf16, false),  TG_SMALL(BM, BN, NS, kFp8, true, kOutBf16, false)
+#define TG_SMALL_KN(BM, BN, NS)                                                            \
+    TG_SMALL(BM, BN, NS, kBf16, false, kOutBf16, true), TG_SMALL(BM, BN, NS, kBf16, false, kOutF32, true)
+
+static const TiledVariant kSmall[] = {
+    TG_SMALL_ALL(64, 64, 5),   // (the K x N swizzle needs 128 columns)
+    TG_SMALL_ALL(64, 128, 4),  TG_SMALL_KN(64, 128, 4),
+    TG_SMALL_ALL(128, 128, 4), TG_SMALL_KN(128, 128, 4),
+};
+
+const TiledVariant *small_variants(int *count)
+{
+    *count = (int)(sizeof(kSmall) / sizeof(kSmall[0]));
+    return kSmall;
 }
 
 const TiledVariant *tiled_variants(int *count)

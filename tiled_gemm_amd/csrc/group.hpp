@@ -137,8 +137,9 @@ template <int OUT>
 __device__ inline void group_enter_inner(TiledArgs &p, int k_rows, int *tm, int *tn)
 {
     const int tiles = p.tiles_m * p.tiles_n;
-    const int v = xcd_run(blockIdx.x, p.grid);
-    const int g = v / tiles, r = v - g * tiles;
+    // Groups in turn, each spread over all XCDs (their rows differ, so an XCD
+    // that owned whole groups would finish early or late).
+    const int g = (int)blockIdx.x / tiles, r = xcd_run((int)blockIdx.x - g * tiles, tiles);
     const int width = p.group_m * p.tiles_n, band = r / width, first = band * p.group_m;
     const int high = min(p.tiles_m - first, p.group_m);
     const int in = r - band * width;

@@ -117,8 +117,6 @@ struct SkinnyArgs {
     const uint8_t *sa_img;
     const uint8_t *sb_img;
     int32_t s_groups;
-    GroupArgs grp;
-    int32_t tiles_n;        // grouped kernels: 32-column tiles of C
 };
 
 struct PreshuffleArgs {
@@ -156,7 +154,7 @@ struct SkinnyVariant {
     hipError_t (*launch_ex)(const SkinnyArgs &, int grid, hipStream_t) = nullptr;   // extended epilogue
 };
 
-// A grouped kernel (group.hpp): tiles of bm rows, 0 < bm <= 64 the skinny ones.
+// A grouped kernel (group.hpp): tiles of bm x bn.
 struct GroupVariant {
     int bm, bn, threads;
     int elem, out;
@@ -166,7 +164,6 @@ struct GroupVariant {
 };
 const GroupVariant *group_dma_variants(int *count);
 const GroupVariant *group_tiled_variants(int *count);
-const GroupVariant *group_skinny_variants(int *count);
 
 constexpr int kMaxGroups = 1024;
 
@@ -212,6 +209,7 @@ constexpr int kSkinnyTileN = 32;
 constexpr int kTiledThreads = 256;
 
 const TiledVariant *tiled_variants(int *count);
+const TiledVariant *small_variants(int *count);  // extended epilogue only, small tiles
 hipError_t launch_split_reduce(const SplitReduceArgs &a, hipStream_t s);
 const TiledVariant *pipe_variants(int *count);
 const TiledVariant *dma_variants(int *count);
