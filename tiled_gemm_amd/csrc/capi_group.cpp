@@ -40,7 +40,7 @@ const tg::GroupVariant *find(const tg::GroupVariant *v, int n, int bm, int elem,
 const tg::GroupVariant *pick(int bm, int elem, int out, int layout)
 {
     int n = 0;
-    const tg::GroupVariant *v = bm == 256 ? tg::group_dma_variants(&n) : tg::group_tiled_variants(&n);
+    const tg::GroupVariant *v = bm == 256 ? tg::group_wide_variants(&n) : tg::group_tiled_variants(&n);
     return find(v, n, bm, elem, out, layout);
 }
 

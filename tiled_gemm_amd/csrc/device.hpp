@@ -495,6 +495,127 @@ __device__ inline void epi_finish4(const EpiView &v, const EpiExt &x, __amdgpu_b
     epi_store4<OUT>(rC, y, voff);
 }
 
+// ---------------------------------------------------------------------------
+// The extended epilogue through LDS.  Unrolled over the accumulators, the
+// epilogue is one copy of the scales, the activations and the stores for every
+// four of them, some 40 KiB of code that runs once per tile: a 256 x 256 tile
+// spent about 15 us fetching it, against 6 us for writing its bytes.  (The
+// accumulators' registers cannot be indexed by a loop.)  So the accumulators
+// go to LDS as they are, BATCH row blocks at a time, into a region that
+// belongs to the wave alone (no barrier), and a loop of one copy reads them
+// back, 16 bytes of one output row per lane: whole lines for the residual's
+// loads and for both stores.  Each lane reads the residual of exactly the
+// elements that it stores, before it stores them, so res may be C itself.
+// The row pitch of 16 FN + 4 floats spreads the 16 rows of a write and the rows
+// of a read over all 64 banks.
+// ---------------------------------------------------------------------------
+template <int FN, int BATCH>
+constexpr int epi_lds_floats() { return BATCH * 16 * (16 * FN + 4); }    // per wave
+
+// acc[i][j]: this lane's 4 columns 16 j + 4 (l / 16) of row l % 16 of block i.
+// Block i's first row is row0 + i * row_step of the tile (and of rC, ex);
+// col0: the wave's first column of C; buf: epi_lds_floats of the wave's own.
+// raw(a): the sums of four accumulators as fp32; row_scale(row): s_a.
+template <int OUT, int BATCH, int FM, int FN, typename Raw, typename RowScale>
+__device__ inline void epi_store_tile(const EpiView &v, const EpiExt &x, __amdgpu_buffer_rsrc_t rC, float *buf,
+                                      const f32x4 (&acc)[FM][FN], int row0, int row_step, int col0, int N,
+                                      uint32_t ldc, Raw raw, RowScale row_scale)
+{
+    static_assert(FM % BATCH == 0, "whole batches");
+    constexpr int COLS = OUT == kOutF32 ? 4 : 8;           // 16 bytes of output per lane and pass
+    constexpr int LANES = 16 * FN / COLS;                   // lanes per row
+    constexpr int ROWS = 64 / LANES;                        // rows per pass
+    constexpr int PITCH = 16 * FN + 4;
+    constexpr int PASSES = BATCH * 16 / ROWS;
+    static_assert(16 % ROWS == 0, "a pass stays inside a block");
+    const int l = (int)(threadIdx.x & 63), q = l >> 4, r16 = l & 15;
+    const int lrow = l / LANES, lcol = (l % LANES) * COLS;
+    const int col = col0 + lcol;
+    float sb[COLS], bz[COLS];
+#pragma unroll
+    for (int c = 0; c < COLS; c += 4) {
+        const f32x4 s = epi_col_scale4(v, col + c), z = epi_bias4(v, col + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            sb[c + e] = s[e];
+            bz[c + e] = z[e];
+        }
+    }
+    const uint32_t coff = col < N ? (uint32_t)col * (OUT == kOutF32 ? 4u : 2u) : kOobOffset;
+    // Tile row of this lane in pass t of the batch that starts at block b.
+    auto row_of = [&](int b, int t) {
+        const int r = t * ROWS + lrow;
+        return row0 + (b + (r >> 4)) * row_step + (r & 15);
+    };
+    auto off_of = [&](int row) { return coff == kOobOffset ? kOobOffset : (uint32_t)row * ldc + coff; };
+#pragma unroll
+    for (int b = 0; b < FM; b += BATCH) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                *(f32x4 *)(buf + (i * 16 + r16) * PITCH + j * 16 + 4 * q) = raw(acc[b + i][j]);
+        __builtin_amdgcn_wave_barrier();
+        int row = row_of(b, 0);
+        float sa = row_scale(row);
+        u32x4 res = x.has_res ? buf_load16(x.rr, off_of(row), 0) : u32x4{0, 0, 0, 0};
+#pragma unroll 1
+        for (int t = 0; t < PASSES; ++t) {
+            // the next pass's scale and residual are on their way while this
+            // one is finished (the last pass fetches its own again)
+            const int nrow = row_of(b, min(t + 1, PASSES - 1));
+            const float nsa = row_scale(nrow);
+            const u32x4 nres = x.has_res ? buf_load16(x.rr, off_of(nrow), 0) : u32x4{0, 0, 0, 0};
+            const float *src = buf + (t * ROWS + lrow) * PITCH + lcol;
+            float y[COLS];
+#pragma unroll
+            for (int c = 0; c < COLS; c += 4) {
+                const f32x4 a = *(const f32x4 *)(src + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    y[c + e] = epi_z1(v, a[e], sa, sb[c + e], bz[c + e]);
+            }
+            auto pack = [&]() {
+                if constexpr (OUT == kOutF32)
+                    return u32x4{__builtin_bit_cast(uint32_t, y[0]), __builtin_bit_cast(uint32_t, y[1]),
+                                 __builtin_bit_cast(uint32_t, y[2]), __builtin_bit_cast(uint32_t, y[3])};
+                else
+                    return u32x4{pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]), pack_bf16x2(y[4], y[5]),
+                                 pack_bf16x2(y[6], y[7])};
+            };
+            const uint32_t voff = off_of(row);
+            if (x.has_pre)
+                buf_store16(x.rp, pack(), voff);
+            // The branch on the activation is outside the columns' loop.
+            if (v.act == kActRelu) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                    y[c] = epi_act(y[c], kActRelu);
+            } else if (v.act == kActSilu) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                    y[c] = epi_act(y[c], kActSilu);
+            } else if (v.act == kActGelu) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c)
+                    y[c] = epi_act(y[c], kActGelu);
+            }
+            if (x.has_res) {
+#pragma unroll
+                for (int c = 0; c < COLS; ++c) {
+                    const uint32_t wd = res[OUT == kOutF32 ? c : c / 2];
+                    y[c] += OUT == kOutF32 ? as_f32(wd) : (c & 1 ? bf16_hi(wd) : bf16_lo(wd));
+                }
+            }
+            buf_store16(rC, pack(), voff);
+            row = nrow;
+            sa = nsa;
+            res = nres;
+        }
+        __builtin_amdgcn_wave_barrier();
+    }
+}
+
 // The same for two columns (s0, s1 hold the sums; on return the outputs).
 template <int OUT>
 __device__ inline void epi_finish2(const EpiView &v, const EpiExt &x, float &s0, float &s1, float sa,

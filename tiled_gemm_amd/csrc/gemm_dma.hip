@@ -31,7 +31,8 @@
 //           stage about to be overwritten has returned).
 //   Epilogue (acc * s_a) * s_b (+ bias, activation) in fp32, RNE to bf16,
 //           buffer stores (rows past M and columns past N dropped).
-#include "group.hpp"
+#include "device.hpp"
+#include "kernels.hpp"
 
 namespace tg {
 
@@ -49,10 +50,9 @@ using dic = std::integral_constant<int, N>;
 
 }  // namespace
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX, bool GRP = false>
-__global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const TiledArgs p0)
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX>
+__global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const TiledArgs p)
 {
-    TiledArgs p = p0;
     static_assert(ELEM == kBf16 || ELEM == kFp8 || (ELEM == kI8 && OUT == kOutBf16),
                   "bf16, fp8 e4m3 or int8 operands");
     // BKN: B stored K x N (C = A * B): a step's K-rows of the tile's 256
@@ -88,23 +88,19 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     // half 0; fp8: B fragments are double-buffered by step parity on the 1 x 8
     // grid, single-buffered (SB, below) on the 2 x 4 grid.
     static_assert(PD >= 1 && (F8 ? PD < FM : PD <= FM), "prefetch distance");
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[DM_LDS];
+    // The extended epilogue's batches of 4 row blocks need 136 KiB.
+    constexpr int EBATCH = FM < 4 ? FM : 4;
+    constexpr int EPI = EX && FN == 4 ? WAVES * epi_lds_floats<FN, EBATCH>() * 4 : 0;
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[DM_LDS > EPI ? DM_LDS : EPI];
 
     const int w = wave_id();
     const int l = lane_id();
     const int q = l >> 4, r16 = l & 15;
     const int wm = w / WGN, wn = w % WGN;
 
+    const SplitK sk = split_k_of(p);
     int tm, tn;
-    if constexpr (GRP && AKM) {
-        group_enter_inner<OUT>(p, KN_ROWS, &tm, &tn);
-    } else if constexpr (GRP) {
-        if (!group_enter<OUT>(p, DM_BM, p.tiles_n, p.group_m, &tm, &tn))
-            return;
-    }
-    const SplitK sk = GRP ? SplitK{0, 0, 0, p.k_tiles, (uint32_t)p.tail_bytes, p.C} : split_k_of(p);
-    if constexpr (!GRP)
-        tile_of_wg(sk.wg, sk.grid, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
+    tile_of_wg(sk.wg, sk.grid, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
     const int m0 = tm * DM_BM, n0 = tn * DM_BN;
     const int rows_a = min(p.M - m0, DM_BM);
     const int rows_b = min(p.N - n0, DM_BN);
@@ -117,11 +113,9 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     // 1-byte ones, the tile's 256 rows of C each.
     constexpr int EA = F8 ? 1 : 2;                       // bytes per element of A
     const uint32_t shA = (uint32_t)sk.kt0 * (AKM ? (uint32_t)KN_ROWS * lda : (uint32_t)kTileKBytes);
-    const bool gather = GRP && !AKM && p.grp.row_index;
     const auto rA = AKM ? make_rsrc((const uint8_t *)p.A + (size_t)m0 * EA + shA,
                                     (uint32_t)((size_t)p.K * lda - (size_t)m0 * EA - shA))
-                    : gather ? make_rsrc(p.A, (uint32_t)p.grp.a_rows * kb)
-                             : make_rsrc((const uint8_t *)p.A + (size_t)m0 * kb + shA, (uint32_t)rows_a * kb - shA);
+                        : make_rsrc((const uint8_t *)p.A + (size_t)m0 * kb + shA, (uint32_t)rows_a * kb - shA);
     // K x N B: the resource starts at column n0 and ends with the matrix, so
     // K-rows past K read zeros; columns past N read neighbouring data or
     // zeros and only feed columns of C that are never stored.
@@ -152,11 +146,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
         } else {
             const int row = pc >> 3;
             const int c = swz_chunk(row, pc & 7);
-            if constexpr (GRP)
-                voffA[r] = gather ? group_a_off(p.grp, p.M, m0 + row, kb, (uint32_t)c * kChunkBytes)
-                                  : (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
-            else
-                voffA[r] = (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
+            voffA[r] = (uint32_t)row * kb + (uint32_t)c * kChunkBytes;
             tailA |= ((uint32_t)(c * kChunkBytes) < tail ? 1u : 0u) << r;
         }
     }
@@ -191,24 +181,6 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     // the offsets need no per-lane selection (no VALU work beside the load).
     auto issue_one = [&](int kt, auto s_c, int idx, auto mask_c) {
         constexpr int S = decltype(s_c)::value;
-        if constexpr (GRP && AKM) {
-            // A group's K-rows may pass 2^32 bytes: the resource itself moves
-            // with the step (64-bit, scalar) and ends with the group, so rows
-            // past it read zeros.
-            const bool a = idx < AR;
-            const uint32_t ld = a ? lda : ldb;
-            const int64_t at = (int64_t)kt * KN_ROWS * ld;
-            const int64_t left = (int64_t)p.K * ld - (int64_t)(a ? m0 * EA : n0 * EB) - at;
-            const uint32_t bytes = (uint32_t)max((int64_t)0, min(left, (int64_t)0x7FFFFFFF));
-            const uint8_t *base = a ? (const uint8_t *)p.A + (size_t)m0 * EA : (const uint8_t *)p.B + (size_t)n0 * EB;
-            const auto r = make_rsrc(base + at, bytes);
-            if (a)
-                buf_load16_to_lds(r, lds + S * DM_STAGE + (idx * WAVES + w) * 1024, voffA[idx], 0);
-            else
-                buf_load16_to_lds(r, lds + S * DM_STAGE + DM_A + ((idx - AR) * WAVES + w) * 1024, voffB[idx - AR], 0);
-            issue_fence();
-            return;
-        }
         if constexpr (!decltype(mask_c)::value) {
             if (idx < AR)
                 buf_load16_to_lds(rA, lds + S * DM_STAGE + (idx * WAVES + w) * 1024, voffA[idx],
@@ -451,11 +423,20 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
 
     // ---- epilogue: row blocks outside, column blocks inside, so a wave
     // writes its adjacent pieces of one C row back to back.
-    const EpiView ev = GRP && !AKM ? group_epi_view(p.epi, p.grp, p.M, p.N) : epi_view(p.epi, p.M, p.N);
+    const EpiView ev = epi_view(p.epi, p.M, p.N);
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)sk.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
     const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
+    if constexpr (EX && FN == 4) {
+        // every wave has read its last fragments before LDS is reused
+        barrier();
+        epi_store_tile<OUT, EBATCH>(ev, ex, rC, reinterpret_cast<float *>(lds) + w * epi_lds_floats<FN, EBATCH>(), acc,
+                                wm * WTM, 16, n0 + wn * WTN, p.N, ldc,
+                                [](f32x4 a) { return I8 ? int_acc_to_f32(a, 1.f) : a; },
+                                [&](int row) { return epi_row_scale(ev, m0 + row); });
+        return;
+    }
     f32x4 sbv[FN], bzv[FN];
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
@@ -466,7 +447,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int row = wm * WTM + i * 16 + r16;
-        const float sa = GRP && !AKM ? group_row_scale(ev, p.grp, p.M, m0 + row) : epi_row_scale(ev, m0 + row);
+        const float sa = epi_row_scale(ev, m0 + row);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = n0 + wn * WTN + j * 16 + 4 * q;
@@ -554,33 +535,6 @@ static const TiledVariant kDma[] = {
     TG_DMA(kFp8, kOutBf16, true, 2, 4, 3),     // 30: fp8 2 x 4, B pre-shuffled
 #endif
 };
-
-// Ragged row groups: the same kernel, entered through group.hpp, with the
-// extended epilogue.
-template <int ELEM, int OUT, bool BPRE, int PD, bool BKN, bool AKM>
-static hipError_t launch_group_dma(const TiledArgs &a, hipStream_t s)
-{
-    hipLaunchKernelGGL((gemm_dma_kernel<ELEM, OUT, BPRE, 2, 4, PD, BKN, AKM, true, true>), dim3(a.grid), dim3(512), 0,
-                       s, a);
-    return hipGetLastError();
-}
-#define TG_GDMA(ELEM, OUT, BPRE, PD, BKN, AKM)                                                      \
-    GroupVariant{DM_BM, DM_BN, 512, ELEM, OUT, BPRE, BKN, AKM, DM_LDS,                               \
-                 &launch_group_dma<ELEM, OUT, BPRE, PD, BKN, AKM>}
-
-static const GroupVariant kGroupDma[] = {
-    TG_GDMA(kBf16, kOutBf16, false, 6, false, false), TG_GDMA(kBf16, kOutF32, false, 4, false, false),
-    TG_GDMA(kBf16, kOutBf16, true, 6, false, false),  TG_GDMA(kBf16, kOutF32, true, 4, false, false),
-    TG_GDMA(kFp8, kOutBf16, false, 2, false, false),  TG_GDMA(kFp8, kOutBf16, true, 2, false, false),
-    TG_GDMA(kBf16, kOutBf16, false, 4, true, false),  TG_GDMA(kBf16, kOutF32, false, 4, true, false),
-    TG_GDMA(kBf16, kOutBf16, false, 2, true, true),   TG_GDMA(kBf16, kOutF32, false, 2, true, true),
-};
-
-const GroupVariant *group_dma_variants(int *count)
-{
-    *count = (int)(sizeof(kGroupDma) / sizeof(kGroupDma[0]));
-    return kGroupDma;
-}
 
 const TiledVariant *dma_variants(int *count)
 {

@@ -56,6 +56,10 @@ struct TiledCfg {
     static_assert(!BKN || (ELEM == kBf16 && !BPRE && KN_CPR >= 16), "K x N B: bf16, staged in LDS");
     static constexpr int STAGE = A_BYTES + B_BYTES;
     static constexpr int LDS = NS * STAGE;
+    // The extended epilogue's batches of row blocks (epi_store_tile).
+    static constexpr int EB = FM < 2 ? FM : 2;
+    static constexpr int EPI = kWaves * epi_lds_floats<FN, EB>() * 4;
+    static constexpr int LDS_EX = LDS > EPI ? LDS : EPI;
     static constexpr int ROUND_BYTES = kTiledThreads * kChunkBytes;   // one 16B load per thread
     static constexpr int A_ROUNDS = A_BYTES / ROUND_BYTES;
     static constexpr int B_ROUNDS = B_BYTES / ROUND_BYTES;
@@ -70,7 +74,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, NS>;
     constexpr bool BREG = Cfg::BREG;
     constexpr int FM = Cfg::FM, FN = Cfg::FN;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[Cfg::LDS];
+    __shared__ __attribute__((aligned(1024))) uint8_t lds[EX ? Cfg::LDS_EX : Cfg::LDS];
 
     const int w = wave_id();
     const int l = lane_id();
@@ -78,7 +82,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
 
     int tm, tn;
     if constexpr (GRP) {
-        if (!group_enter<OUT>(p, BM, p.tiles_n, p.group_m, &tm, &tn))
+        if (!group_enter<OUT, false>(p, BM, p.tiles_n, p.group_m, &tm, &tn))
             return;
     } else {
         tile_of_wg(blockIdx.x, p.grid, p.tiles_m, p.tiles_n, p.group_m, &tm, &tn);
@@ -331,20 +335,27 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
     const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
+    if constexpr (EX) {
+        constexpr int EB = Cfg::EB;
+        __syncthreads();                       // every wave has read its last fragments before LDS is reused
+        epi_store_tile<OUT, EB>(ev, ex, rC, reinterpret_cast<float *>(lds) + w * epi_lds_floats<FN, EB>(), acc,
+                                wm * Cfg::WTM, 16, n0 + wn * Cfg::WTN, p.N, ldc, [](f32x4 a) { return a; },
+                                [&](int row) {
+                                    return GRP ? group_row_scale(ev, p.grp, p.M, m0 + row)
+                                               : epi_row_scale(ev, m0 + row);
+                                });
+        return;
+    }
     // Row blocks outside, column blocks inside: adjacent pieces of a C row
     // leave back to back and merge in the L2 into whole lines.
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
         const int row = wm * Cfg::WTM + i * 16 + r16;
-        const float sa = GRP ? group_row_scale(ev, p.grp, p.M, m0 + row) : epi_row_scale(ev, m0 + row);
+        const float sa = epi_row_scale(ev, m0 + row);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
             const int col = n0 + wn * Cfg::WTN + j * 16 + 4 * q;
             const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * OB : kOobOffset;
-            if constexpr (EX) {
-                epi_finish4<OUT>(ev, ex, rC, acc[i][j], sa, epi_col_scale4(ev, col), epi_bias4(ev, col), voff);
-                continue;
-            }
             const f32x4 v = epi_apply4(ev, acc[i][j], sa, epi_col_scale4(ev, col), epi_bias4(ev, col));
             if constexpr (OUT == kOutF32) {
                 buf_store16(rC, __builtin_bit_cast(u32x4, v), voff);
@@ -405,7 +416,7 @@ static hipError_t launch_group_tiled(const TiledArgs &a, hipStream_t s)
 }
 #define TG_GTILED(BM, BN, WGM, NS, ELEM, BPRE, OUT, BKN)                                   \
     GroupVariant{BM, BN, kTiledThreads, ELEM, OUT, BPRE, BKN, false,                        \
-                 TiledCfg<BM, BN, WGM, 4 / WGM, ELEM, BPRE, OUT, BKN, NS>::LDS,             \
+                 TiledCfg<BM, BN, WGM, 4 / WGM, ELEM, BPRE, OUT, BKN, NS>::LDS_EX,          \
                  &launch_group_tiled<BM, BN, WGM, NS, ELEM, BPRE, OUT, BKN>}
 #define TG_GTILED_ALL(...)                                                                 \
     TG_GTILED(__VA_ARGS__, kBf16, false, kOutBf16, false), TG_GTILED(__VA_ARGS__, kBf16, false, kOutF32, false), \

@@ -24,8 +24,22 @@ struct GroupScan {
     int total;          // tiles of all groups (the same in every lane)
 };
 
-// Tiles of `tile` rows each; tiles never cross a group.
-__device__ inline GroupScan group_scan(const int32_t *off, int groups, int rows, int tile)
+// How many tiles a group of n rows has; tiles never cross a group.
+struct TilesAll {                   // of `tile` rows, the last one ragged
+    int tile;
+    __device__ int operator()(int n) const { return (n + tile - 1) / tile; }
+};
+struct TilesHeavy {                 // those with more than half their rows
+    int tile;
+    __device__ int operator()(int n) const { return (n + tile / 2 - 1) / tile; }
+};
+struct TilesLight {                 // the last one, where it has at most half
+    int tile;
+    __device__ int operator()(int n) const { return TilesAll{tile}(n) - TilesHeavy{tile}(n); }
+};
+
+template <typename Count>
+__device__ inline GroupScan group_scan_by(const int32_t *off, int groups, int rows, Count count)
 {
     GroupScan s;
     const int l = (int)(threadIdx.x & 63);
@@ -35,7 +49,7 @@ __device__ inline GroupScan group_scan(const int32_t *off, int groups, int rows,
         const int g = l * s.per + i;
         if (g < groups) {
             const int lo = group_lo(off, g, rows);
-            n += (group_hi(off, g, rows, lo) - lo + tile - 1) / tile;
+            n += count(group_hi(off, g, rows, lo) - lo);
         }
     }
     int x = n;
@@ -50,6 +64,11 @@ __device__ inline GroupScan group_scan(const int32_t *off, int groups, int rows,
     return s;
 }
 
+__device__ inline GroupScan group_scan(const int32_t *off, int groups, int rows, int tile)
+{
+    return group_scan_by(off, groups, rows, TilesAll{tile});
+}
+
 struct GroupTile {
     int g;              // group
     int lo, hi;         // its rows
@@ -58,7 +77,9 @@ struct GroupTile {
 };
 
 // The group that holds tile t (0 <= t < s.total; the same t in every lane).
-__device__ inline GroupTile group_find(const GroupScan &s, const int32_t *off, int groups, int rows, int tile, int t)
+template <typename Count>
+__device__ inline GroupTile group_find_by(const GroupScan &s, const int32_t *off, int groups, int rows, Count count,
+                                          int t)
 {
     GroupTile r;
     const unsigned long long m = __ballot(s.incl > t);
@@ -67,13 +88,13 @@ __device__ inline GroupTile group_find(const GroupScan &s, const int32_t *off, i
     r.g = lane * s.per;
     r.lo = group_lo(off, r.g, rows);
     r.hi = group_hi(off, r.g, rows, r.lo);
-    r.tiles = (r.hi - r.lo + tile - 1) / tile;
+    r.tiles = count(r.hi - r.lo);
     for (int i = 1; i < s.per && t >= r.first + r.tiles; ++i) {
         r.first += r.tiles;
         ++r.g;
         r.lo = group_lo(off, r.g, rows);
         r.hi = group_hi(off, r.g, rows, r.lo);
-        r.tiles = (r.hi - r.lo + tile - 1) / tile;
+        r.tiles = count(r.hi - r.lo);
     }
     r.g = __builtin_amdgcn_readfirstlane(r.g);
     r.lo = __builtin_amdgcn_readfirstlane(r.lo);
@@ -81,6 +102,11 @@ __device__ inline GroupTile group_find(const GroupScan &s, const int32_t *off, i
     r.first = __builtin_amdgcn_readfirstlane(r.first);
     r.tiles = __builtin_amdgcn_readfirstlane(r.tiles);
     return r;
+}
+
+__device__ inline GroupTile group_find(const GroupScan &s, const int32_t *off, int groups, int rows, int tile, int t)
+{
+    return group_find_by(s, off, groups, rows, TilesAll{tile}, t);
 }
 
 // Workgroup w of `total` renumbered so that each XCD (w % 8) gets a contiguous
@@ -94,22 +120,39 @@ __device__ inline int xcd_run(int w, int total)
 // Restricts a grouped kernel's arguments to the group of this workgroup's
 // tile: A, C, M and the epilogue's vectors to the group's rows, B to the
 // group's matrix.  *tm, *tn: the tile inside the group.  False: no tile left.
-template <int OUT, typename Args>
-__device__ inline bool group_enter(Args &p, int bm, int tiles_n, int group_m, int *tm, int *tn)
+// LIGHT: the groups' last tiles with at most half their rows, which such a
+// kernel finishes in about half the time, come after all others, so that
+// they and not whole tiles fill the last round of workgroups.
+template <int OUT, bool LIGHT>
+__device__ inline bool group_enter(TiledArgs &p, int bm, int tiles_n, int group_m, int *tm, int *tn)
 {
-    const GroupScan s = group_scan(p.grp.offsets, p.grp.groups, p.grp.rows, bm);
+    const int32_t *off = p.grp.offsets;
+    const int groups = p.grp.groups, rows = p.grp.rows;
+    const GroupScan s = LIGHT ? group_scan_by(off, groups, rows, TilesHeavy{bm}) : group_scan(off, groups, rows, bm);
     // offsets that run backwards may count more tiles than 32 bits hold work for
     const int total = min((int64_t)s.total * tiles_n, (int64_t)gridDim.x);
-    if ((int)blockIdx.x >= total)
-        return false;
-    const int v = xcd_run(blockIdx.x, total);
-    const GroupTile g = group_find(s, p.grp.offsets, p.grp.groups, p.grp.rows, bm, v / tiles_n);
-    const int r = v - g.first * tiles_n;
-    const int width = group_m * tiles_n, band = r / width, first = band * group_m;
-    const int high = min(g.tiles - first, group_m);
-    const int in = r - band * width;
-    *tm = first + in % high;
-    *tn = in / high;
+    GroupTile g;
+    if ((int)blockIdx.x < total) {
+        const int v = xcd_run(blockIdx.x, total);
+        g = LIGHT ? group_find_by(s, off, groups, rows, TilesHeavy{bm}, v / tiles_n)
+                  : group_find(s, off, groups, rows, bm, v / tiles_n);
+        const int r = v - g.first * tiles_n;
+        const int width = group_m * tiles_n, band = r / width, first = band * group_m;
+        const int high = min(g.tiles - first, group_m);
+        const int in = r - band * width;
+        *tm = first + in % high;
+        *tn = in / high;
+    } else {
+        if constexpr (!LIGHT)
+            return false;
+        const GroupScan s2 = group_scan_by(off, groups, rows, TilesLight{bm});
+        const int k = (int)blockIdx.x - total;
+        if (k >= (int64_t)s2.total * tiles_n)
+            return false;
+        g = group_find_by(s2, off, groups, rows, TilesLight{bm}, k / tiles_n);
+        *tm = TilesHeavy{bm}(g.hi - g.lo);
+        *tn = k - g.first * tiles_n;
+    }
     constexpr size_t OB = OUT == kOutF32 ? 4 : 2;
     const size_t c_off = (size_t)g.lo * (size_t)p.N * OB;
     if (p.grp.row_index) {

@@ -162,7 +162,7 @@ struct GroupVariant {
     int lds_bytes;
     hipError_t (*launch)(const TiledArgs &, hipStream_t);
 };
-const GroupVariant *group_dma_variants(int *count);
+const GroupVariant *group_wide_variants(int *count);
 const GroupVariant *group_tiled_variants(int *count);
 
 constexpr int kMaxGroups = 1024;
