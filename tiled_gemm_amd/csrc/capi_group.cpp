@@ -285,16 +285,17 @@ int gemm_group_run(const gemm_group_plan *plan, const void *A, const void *B, vo
 
 namespace {
 
-// One block for up to kSortOne slots; above, blocks of at least that many,
-// at most kSortBlocks of them (each block reads every block's counts).
+// One block, and one launch, for up to kSortOne slots; above, blocks of 1024
+// slots, one per thread, or more, so that there is at most one per CU (each
+// block reads every block's counts).
 constexpr int64_t kSortOne = 4096;
 constexpr int64_t kSortBlocks = 256;
 constexpr int64_t kSortStep = 1024;      // 16 waves x 64 slots
 
 void sort_split(int64_t slots, int32_t *blocks, int32_t *block_slots)
 {
-    int64_t b = (slots + kSortOne - 1) / kSortOne;
-    b = b < 1 ? 1 : (b > kSortBlocks ? kSortBlocks : b);
+    int64_t b = slots <= kSortOne ? 1 : (slots + kSortStep - 1) / kSortStep;
+    b = b > kSortBlocks ? kSortBlocks : b;
     int64_t per = (slots + b - 1) / b;
     per = (per + kSortStep - 1) / kSortStep * kSortStep;
     per = per < kSortStep ? kSortStep : per;

@@ -512,6 +512,15 @@ __device__ inline void epi_finish4(const EpiView &v, const EpiExt &x, __amdgpu_b
 template <int FN, int BATCH>
 constexpr int epi_lds_floats() { return BATCH * 16 * (16 * FN + 4); }    // per wave
 
+// SiLU with the hardware's exponential and reciprocal (each within an ulp or
+// so): z / (1 + 2^(-z log2 e)).  The error of the exponent's argument is at most
+// |z| 2^-23 relative to e^-z, far below the epilogue's 2^-20 |z|; the limits at
+// the infinities are those of the division.
+__device__ inline float epi_silu(float z)
+{
+    return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+}
+
 // acc[i][j]: this lane's 4 columns 16 j + 4 (l / 16) of row l % 16 of block i.
 // Block i's first row is row0 + i * row_step of the tile (and of rC, ex);
 // col0: the wave's first column of C; buf: epi_lds_floats of the wave's own.
@@ -594,7 +603,7 @@ __device__ inline void epi_store_tile(const EpiView &v, const EpiExt &x, __amdgp
             } else if (v.act == kActSilu) {
 #pragma unroll
                 for (int c = 0; c < COLS; ++c)
-                    y[c] = epi_act(y[c], kActSilu);
+                    y[c] = epi_silu(y[c]);
             } else if (v.act == kActGelu) {
 #pragma unroll
                 for (int c = 0; c < COLS; ++c)

@@ -139,28 +139,34 @@ __device__ inline void group_tile(const TiledArgs &p, int tm, int tn, uint8_t *l
     };
 
     // ---- fragments (see gemm_dma.hip for the lane orders)
-    auto tr_frag = [&](const uint8_t *base, int col, int h) -> u32x4 {   // K x M or K x N operand, two transpose reads
-        const int c = (col * 2) >> 4, off = (col * 2) & 15;
-        u32x2 t2[2];
+    // K x M or K x N operand: two transpose reads, of K-rows k = 32 h + 8 q + 4 t
+    // + r16 / 4 of the step, chunk c ^ bkn_swz(k) of the 512-byte row.  The swizzle
+    // has the same value for every h and t, and flips bits 1 to 3 of the chunk,
+    // so four offsets per operand serve all its blocks; the rest are constants.
+    uint32_t trA[4], trB[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const int k = 32 * h + 8 * q + 4 * t + (r16 >> 2);
-            t2[t] = lds_read_tr16(base + k * 512 + ((c ^ bkn_swz(k)) << 4) + off);
-        }
-        return u32x4{t2[0].x, t2[0].y, t2[1].x, t2[1].y};
+    for (int x = 0; x < 4; ++x) {
+        const int s = bkn_swz(8 * q + (r16 >> 2)), b = (r16 & 3) >> 1;
+        const uint32_t lane = (uint32_t)(4096 * q + 512 * (r16 >> 2) + 8 * (r16 & 1));
+        trA[x] = lane + (uint32_t)(((4 * x + 2 * wm + b) ^ s) << 4);          // row block i: x = i % 4, + 256 (i / 4)
+        trB[x] = lane + (uint32_t)(((8 * wn + 2 * x + b) ^ s) << 4) + GM_A;   // column block x of the wave
+    }
+    auto tr_frag = [&](const uint8_t *at, int h) -> u32x4 {
+        const u32x2 t0 = lds_read_tr16(at + h * 16384), t1 = lds_read_tr16(at + h * 16384 + 2048);
+        return u32x4{t0.x, t0.y, t1.x, t1.y};
     };
     auto a16 = [&](int s, int i, int h) -> u32x4 {
         const uint8_t *sA = lds + s * GM_STAGE;
         if constexpr (AKM)
-            return tr_frag(sA, (i * GM_WGM + wm) * 16 + 4 * (r16 & 3), h);
+            return tr_frag(sA + trA[i & 3] + (i >> 2) * 256, h);
         const int row = row_of(i);
         return lds_load16(sA + row * kTileKBytes + swz_chunk(row, h * 4 + q) * kChunkBytes);
     };
     auto b16 = [&](int s, int j, int h) -> u32x4 {
+        if constexpr (BKN)
+            return tr_frag(lds + s * GM_STAGE + trB[j], h);
         const uint8_t *sB = lds + s * GM_STAGE + GM_A;
         const int nb = wn * FN + j;
-        if constexpr (BKN)
-            return tr_frag(sB, nb * 16 + 4 * (r16 & 3), h);
         if constexpr (BPRE)
             return lds_load16(sB + (nb * 2 + h) * 1024 + l * 16);
         const int row = nb * 16 + r16;

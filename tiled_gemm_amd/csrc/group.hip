@@ -55,6 +55,7 @@ __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const SortArg
 {
     __shared__ int32_t hist[kSortWaves][kMaxGroups];    // per wave: counts, then the next row of each group
     __shared__ int32_t wave_sum[kSortWaves];
+    __shared__ int32_t part_total[kSortThreads], part_before[kSortThreads];
     const int tid = threadIdx.x, w = wave_id(), l = lane_id();
     volatile int32_t *mine = hist[w];
     for (int g = l; g < a.groups; g += 64)
@@ -73,20 +74,34 @@ __global__ __launch_bounds__(kSortThreads) void group_place_kernel(const SortArg
             mine[id] = mine[id] + __popcll(m);
     }
     __syncthreads();
-    // Thread g: group g's rows in this block, in the blocks before it and in
-    // all of them.
+    // Thread g: group g's rows in all blocks and in the blocks before this one.
+    // With several blocks all threads share the reading: thread p * 2^id_bits + g
+    // adds up every (1024 / 2^id_bits)-th block from block p on.
     int total = 0, before = 0;
-    if (tid < a.groups) {
-        if (a.blocks > 1) {
-            for (int b = 0; b < a.blocks; ++b) {
-                const int c = a.counts[(size_t)b * a.groups + tid];
-                total += c;
-                before += b < (int)blockIdx.x ? c : 0;
+    if (a.blocks > 1) {
+        const int wide = 1 << a.id_bits, parts = kSortThreads / wide;
+        const int g = tid & (wide - 1), part = tid >> a.id_bits;
+        int sum = 0, early = 0;
+        if (g < a.groups) {
+#pragma unroll 8
+            for (int b = part; b < a.blocks; b += parts) {
+                const int c = a.counts[(size_t)b * a.groups + g];
+                sum += c;
+                early += b < (int)blockIdx.x ? c : 0;
             }
-        } else {
-            for (int ww = 0; ww < kSortWaves; ++ww)
-                total += hist[ww][tid];
         }
+        part_total[tid] = sum;
+        part_before[tid] = early;
+        __syncthreads();
+        if (tid < a.groups) {
+            for (int i = 0; i < parts; ++i) {
+                total += part_total[(i << a.id_bits) + tid];
+                before += part_before[(i << a.id_bits) + tid];
+            }
+        }
+    } else if (tid < a.groups) {
+        for (int ww = 0; ww < kSortWaves; ++ww)
+            total += hist[ww][tid];
     }
     int x = total;                                         // inclusive sum over the groups
 #pragma unroll
