@@ -318,11 +318,17 @@ static hipError_t launch_group(const TiledArgs &a, hipStream_t s)
                  &launch_group<ELEM, OUT, BPRE, PD, BKN, AKM>}
 
 static const GroupVariant kGroup[] = {
-    TG_GROUP(kBf16, kOutBf16, false, 6, false, false), TG_GROUP(kBf16, kOutF32, false, 4, false, false),
+    // PD: the loads of a step are spread over its last PD groups and waited for
+    // PD groups before the end of the next, so a small PD leaves them more time
+    // and a large one the fragments.  Measured (16 groups of 2048 rows, us):
+    // transposed A and B, 4 / 2 / 1: 779 / 635 / 589; B K x N, 5 / 4 / 2: 552 /
+    // 533 / 520; fp8 pre-shuffled, 2 / 1: 333 / 317; bf16 N x K, 6 / 5 / 3: 446 /
+    // 442 / 454.
+    TG_GROUP(kBf16, kOutBf16, false, 5, false, false), TG_GROUP(kBf16, kOutF32, false, 4, false, false),
     TG_GROUP(kBf16, kOutBf16, true, 6, false, false),  TG_GROUP(kBf16, kOutF32, true, 4, false, false),
-    TG_GROUP(kFp8, kOutBf16, false, 2, false, false),  TG_GROUP(kFp8, kOutBf16, true, 2, false, false),
-    TG_GROUP(kBf16, kOutBf16, false, 4, true, false),  TG_GROUP(kBf16, kOutF32, false, 4, true, false),
-    TG_GROUP(kBf16, kOutBf16, false, 2, true, true),   TG_GROUP(kBf16, kOutF32, false, 2, true, true),
+    TG_GROUP(kFp8, kOutBf16, false, 1, false, false),  TG_GROUP(kFp8, kOutBf16, true, 1, false, false),
+    TG_GROUP(kBf16, kOutBf16, false, 2, true, false),  TG_GROUP(kBf16, kOutF32, false, 2, true, false),
+    TG_GROUP(kBf16, kOutBf16, false, 1, true, true),   TG_GROUP(kBf16, kOutF32, false, 1, true, true),
 };
 
 const GroupVariant *group_wide_variants(int *count)

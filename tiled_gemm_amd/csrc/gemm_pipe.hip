@@ -485,7 +485,19 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
     constexpr int OB = OUT == kOutF32 ? 4 : 2;
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)sk.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
-    const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
+    if constexpr (EX) {
+        // Through LDS, once every wave's loads have landed and its last
+        // fragments are read.
+        static_assert(Cfg::WAVES * epi_lds_floats<BP_FN, 4>() * 4 <= Cfg::LDS, "the batches fit the stages");
+        const EpiExt ex = epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
+        __builtin_amdgcn_s_waitcnt(0);
+        barrier();
+        epi_store_tile<OUT, 4>(ev, ex, rC, reinterpret_cast<float *>(lds) + w * epi_lds_floats<BP_FN, 4>(), acc,
+                               wm * BP_WTM, 16, n0 + wn * BP_WTN, p.N, ldc,
+                               [](f32x4 a) { return INT ? int_acc_to_f32(a, W4 ? 0.0625f : 1.f) : a; },
+                               [&](int row) { return epi_row_scale(ev, m0 + row); });
+        return;
+    }
     f32x4 sbv[BP_FN], bzv[BP_FN];
 #pragma unroll
     for (int j = 0; j < BP_FN; ++j) {
@@ -502,10 +514,6 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
             const int col = n0 + wn * BP_WTN + j * 16 + 4 * q;
             const uint32_t voff = col < p.N ? (uint32_t)row * ldc + (uint32_t)col * OB : kOobOffset;
             const f32x4 a = INT ? int_acc_to_f32(acc[i][j], W4 ? 0.0625f : 1.f) : acc[i][j];
-            if constexpr (EX) {
-                epi_finish4<OUT>(ev, ex, rC, a, sa, sbv[j], bzv[j], voff);
-                continue;
-            }
             const f32x4 v = epi_apply4(ev, a, sa, sbv[j], bzv[j]);
             if constexpr (OUT == kOutF32)
                 buf_store16(rC, __builtin_bit_cast(u32x4, v), voff);
