@@ -526,3 +526,19 @@ def test_expert_layer_in_a_graph():
         torch.cuda.synchronize()
         for name in ("off", "row", "y", "dx", "dw", "dw1", "db1", "dw2"):
             assert torch.equal(getattr(a, name), getattr(b, name)), name
+
+
+@pytest.mark.parametrize("tile", [32, 64, 128, 256])
+def test_capacity_far_above_the_rows(tile):
+    """Room for 9000 rows, 0 to 70 of them used: what lies behind is left alone."""
+    rng = np.random.default_rng(tile)
+    a, b = ints(rng, (9000, 64), -3, 3), ints(rng, (4, 48, 64), -3, 3)
+    A, B = dev(a, torch.bfloat16), dev(b, torch.bfloat16)
+    with tg.GroupPlan(4, 9000, 48, 64, F32O, tg.GEMM_LAYOUT_BT, tile_rows=tile) as p:
+        for off in ([0, 0, 0, 0, 0], [0, 0, 1, 1, 1], [0, 33, 33, 69, 70]):
+            C = torch.full((9000, 48), 5.0, dtype=torch.float32, device="cuda")
+            grouped(p, A, B, C, i32(off))
+            want = np.full((9000, 48), 5.0)
+            for g in range(4):
+                want[off[g]:off[g + 1]] = a[off[g]:off[g + 1]] @ b[g].T
+            assert np.array_equal(host(C), want)

@@ -349,11 +349,16 @@ __device__ inline float act_slope(float z)
         return z > 0.f ? 1.f : 0.f;
     } else if constexpr (ACT == kActSilu) {
         const float c = z < -100.f ? -100.f : (z > 100.f ? 100.f : z);
-        const float p = 1.f / (1.f + expf(-c));
+        // the hardware's exponential and reciprocal, each within an ulp or so:
+        // with expf and a division the kernel was bound by its arithmetic
+        // (8192 x 8192 bf16 with d_bias: 92 us; 87 so)
+        const float p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(c * -1.44269504088896340736f));
         return p * (1.f + c * (1.f - p));
     } else if constexpr (ACT == kActGelu) {
         const float c = z < -100.f ? -100.f : (z > 100.f ? 100.f : z);
-        return 0.5f * (1.f + erff(c * 0.70710678118654752440f)) + c * 0.39894228040143267794f * expf(-0.5f * c * c);
+        // phi's exponent on the hardware's 2^x: c^2 / 2 log2 e
+        const float phi = 0.39894228040143267794f * __builtin_amdgcn_exp2f(c * c * -0.72134752044448170368f);
+        return 0.5f * (1.f + erff(c * 0.70710678118654752440f)) + c * phi;
     }
     return 1.f;
 }

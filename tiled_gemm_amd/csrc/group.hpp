@@ -128,6 +128,12 @@ __device__ inline bool group_enter(TiledArgs &p, int bm, int tiles_n, int group_
 {
     const int32_t *off = p.grp.offsets;
     const int groups = p.grp.groups, rows = p.grp.rows;
+    // The launch covers the rows there is room for.  What offsets[groups] alone
+    // rules out leaves before the scan (a capacity of several times the rows
+    // would otherwise pay a scan for every workgroup too many).
+    const int64_t most = ((int64_t)group_lo(off, groups, rows) + (int64_t)groups * (bm - 1)) / bm * tiles_n;
+    if ((int64_t)blockIdx.x >= most)
+        return false;
     const GroupScan s = LIGHT ? group_scan_by(off, groups, rows, TilesHeavy{bm}) : group_scan(off, groups, rows, bm);
     // offsets that run backwards may count more tiles than 32 bits hold work for
     const int total = min((int64_t)s.total * tiles_n, (int64_t)gridDim.x);
