@@ -499,8 +499,8 @@ __device__ inline void epi_finish4(const EpiView &v, const EpiExt &x, __amdgpu_b
 // The extended epilogue through LDS.  Unrolled over the accumulators, the
 // epilogue is one copy of the scales, the activations and the stores for every
 // four of them, some 40 KiB of code that runs once per tile: a 256 x 256 tile
-// spent about 15 us fetching it, against 6 us for writing its bytes.  (The
-// accumulators' registers cannot be indexed by a loop.)  So the accumulators
+// with nothing to multiply took 20 us so, and 9 us in this form (writing its
+// bytes takes 6).  (The accumulators' registers cannot be indexed by a loop.)  So the accumulators
 // go to LDS as they are, BATCH row blocks at a time, into a region that
 // belongs to the wave alone (no barrier), and a loop of one copy reads them
 // back, 16 bytes of one output row per lane: whole lines for the residual's
