@@ -12,8 +12,8 @@ Q, R, S, T, U, V = (P + (i << 34) for i in range(1, 7))
 
 
 @pytest.mark.parametrize("groups,M,layout,tile", [(64, 64, PRE, 32), (64, 24 * 64, BT, 32), (8, 25 * 8, BT, 64),
-                                                  (8, 56 * 8, PRE, 64), (8, 57 * 8, BT, 128), (4, 4 * 384, BT, 128),
-                                                  (4, 4 * 385, BT, 256), (4, 1, BN, 32), (4, 4096, BN, 256)])
+                                                  (8, 96 * 8, PRE, 64), (8, 97 * 8, BT, 128), (4, 4 * 192, BT, 128),
+                                                  (4, 4 * 193, BT, 256), (4, 1, BN, 32), (4, 4096, BN, 256)])
 def test_tile_rule_and_grid(groups, M, layout, tile):
     with tg.GroupPlan(groups, M, 528, 256, BF, layout) as p:
         info = p.info()

@@ -47,15 +47,17 @@ const tg::GroupVariant *pick(int bm, int elem, int out, int layout)
 // Rows per tile from the mean rows per group, M being the rows there is room
 // for.  Up to 24 rows (decode) the 32-row tiles stream the active experts'
 // weights at the rate of a copy; larger tiles read the same weights with fewer
-// workgroups in flight.  Measured (bf16, 64 groups, N 2048, K 1024, us for
-// tiles of 32 / 64 / 128 / 256): mean 1: 32 / 38 / 48 / 91; mean 32: 58 / 55 /
-// 63 / 99; mean 64: 77 / 70 / 64 / 99; mean 200: 173 / 131 / 127 / 145.
+// workgroups in flight.  Measured on uneven groups (us for tiles of 32 / 64 /
+// 128 / 256), bf16, 64 groups, N 2048, K 1024: mean 8: 44 / 43 / 47 / 52; mean
+// 48: 60 / 55 / 61 / 66; mean 120: 106 / 85 / 81 / 83; 16 groups, N 2048, K 4096:
+// mean 80: 74 / 59 / 70 / 94; mean 170: 121 / 100 / 76 / 103; mean 300 (64 / 128 /
+// 256): 147 / 139 / 115; mean 1000: 392 / 319 / 291.
 int default_tile(int groups, int64_t M, int layout)
 {
     if (layout == GEMM_LAYOUT_AT_BN)
         return 256;
     const int64_t mean = (M + groups - 1) / groups;
-    return mean <= 24 ? 32 : (mean <= 56 ? 64 : (mean <= 384 ? 128 : 256));
+    return mean <= 24 ? 32 : (mean <= 96 ? 64 : (mean <= 192 ? 128 : 256));
 }
 
 }  // namespace
