@@ -258,7 +258,7 @@ __device__ inline void group_tile(const TiledArgs &p, int tm, int tn, uint8_t *l
 #pragma unroll
     for (int t = 0; t < PD; ++t)
         load_group(0, t);
-    // Steps run in pairs; a step past nk multiplies zeros.
+    // Steps run in pairs, one per stage.
     const int nfull = tail == (uint32_t)kTileKBytes ? nk : nk - 1;
     int kt = 0;
     for (; kt + 1 < nfull - 2; kt += 2) {
@@ -267,6 +267,8 @@ __device__ inline void group_tile(const TiledArgs &p, int tm, int tn, uint8_t *l
     }
     for (; kt < nk; kt += 2) {
         step(kt, s0{}, masked{});
+        if (kt + 1 == nk)
+            break;
         step(kt + 1, s1{}, masked{});
     }
     __builtin_amdgcn_s_waitcnt(0);
