@@ -248,7 +248,9 @@ __device__ inline void group_tile(const TiledArgs &p, int tm, int tn, uint8_t *l
 #pragma unroll
     for (int idx = 0; idx < NL; ++idx)
         issue_one(1, s1{}, idx, masked{});
-    __builtin_amdgcn_s_waitcnt(0);
+    // Step 0 has landed; step 1 is waited for inside step 0.
+    static_assert(NL < 16, "the low bits of vmcnt");
+    __builtin_amdgcn_s_waitcnt(((kWaitVmcnt0 & ~0xC00F) | NL) & 0xC07F);
     barrier();
     if constexpr (F8) {
 #pragma unroll
