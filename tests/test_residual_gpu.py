@@ -120,6 +120,25 @@ def test_bit_exact_transposed_layouts(layout, kernel, out):
     assert torch.equal(C, as_c(np.maximum(z, 0.0) + r, out)) and torch.equal(Z, as_c(z, out))
 
 
+@pytest.mark.parametrize("layout", ["bn", "at", "at_bn"])
+@pytest.mark.parametrize("dtype", ["e4m3", "i8"])
+def test_bit_exact_transposed_8bit(layout, dtype):
+    M, N, K = 272, 304, 1088
+    rng = np.random.default_rng(9)
+    a, b = rng.integers(-4, 5, (M, K)).astype(np.float64), rng.integers(-4, 5, (N, K)).astype(np.float64)
+    r, bias = rng.integers(-64, 65, (M, N)).astype(np.float64), rng.integers(-8, 9, N).astype(np.float64)
+    et = torch.float8_e4m3fn if dtype == "e4m3" else torch.int8
+    A = as_c(a.T if layout.startswith("at") else a, "f32").contiguous().to(et)
+    B = as_c(b.T if layout.endswith("bn") else b, "f32").contiguous().to(et)
+    R, dbias = as_c(r, "bf16"), torch.tensor(bias, dtype=torch.float32, device="cuda")
+    C, Z = torch.empty_like(R), torch.empty_like(R)
+    with tg.Plan(M, N, K, CODE[dtype, "bf16"], tg.LAYOUTS[layout]) as p:
+        call(p, layout, A, B, C, residual=R.data_ptr(), preact=Z.data_ptr(), bias=dbias.data_ptr(),
+             epilogue=tg.GEMM_EPI_BIAS_RELU)
+    z = a @ b.T + bias
+    assert torch.equal(C, as_c(np.maximum(z, 0.0) + r, "bf16")) and torch.equal(Z, as_c(z, "bf16"))
+
+
 @pytest.mark.parametrize("kind", ["bias_silu", "bias_gelu"])
 @pytest.mark.parametrize("M,layout,kernel,split", [(300, "bt", "auto", 0), (300, "bt", "tile256", 0),
                                                   (20, "bt_preshuffled", "auto", 0), (300, "bt", "auto", 4),

@@ -497,7 +497,9 @@ static const TiledVariant kDma[] = {
     TG_DMA(kBf16, kOutBf16, false, 2, 4, 6),   // B N x K
     TG_DMA(kBf16, kOutF32, false, 2, 4, 4),
     TG_DMA(kFp8, kOutBf16, false, 2, 4, 2),    // fp8, B N x K
-    TG_DMA(kFp8, kOutF32, false, 2, 4, 2),
+    // fp8 with fp32 output: split-K partial tiles only, no extended epilogue
+    TiledVariant{DM_BM, DM_BN, 2, 4, kFp8, kOutF32, false, DM_LDS, 2,
+                 &launch_dma<kFp8, kOutF32, false, 2, 4, 2, false, false>},
     TG_DMA(kI8, kOutBf16, false, 2, 4, 2),     // int8, B N x K
     TG_DMA_KN(kOutBf16, 2, 4, 4),              // B stored K x N
     TG_DMA_KN(kOutF32, 2, 4, 4),
