@@ -1,0 +1,92 @@
+"""Sizes at the ends of what the residual epilogue and the grouped operators
+accept: an empty inner size, and the largest ones.  Every expected value is
+exact (small integers, powers of two), so the comparisons are equalities."""
+import numpy as np
+import pytest
+import torch
+
+import tiled_gemm_amd as tg
+
+pytestmark = pytest.mark.gpu
+
+BF, F32O, E4, I8 = tg.GEMM_BF16_OUT_BF16, tg.GEMM_BF16_OUT_F32, tg.GEMM_E4M3_OUT_BF16, tg.GEMM_I8_OUT_BF16
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def ctype(code):
+    return torch.float32 if code == F32O else torch.bfloat16
+
+
+def small_ints(shape, lo, hi, seed, dtype=torch.float32):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(lo, hi + 1, shape, generator=g, device="cuda").to(dtype)
+
+
+# ------------------------------------------------------------------ K = 0
+# C = act(bias) (+ residual), and nothing of A or B is read.  N gives several
+# column tiles of every family.
+
+GROUPED = ([(code, lay, tile) for code in (BF, F32O) for lay in ("bt", "bt_preshuffled", "bn") for tile in (32, 64, 128, 256)] +
+           [(E4, lay, tile) for lay in ("bt", "bt_preshuffled") for tile in (32, 64, 128, 256)])
+
+
+@pytest.mark.parametrize("code,layout,tile", GROUPED)
+@pytest.mark.parametrize("gather", [False, True])
+def test_grouped_product_with_no_inner_size(code, layout, tile, gather):
+    print("case K=0 grouped", code, layout, tile, gather, flush=True)
+    groups, M, N, off = 3, 400, 528, [1, 300, 300, 390]
+    dt = ctype(code)
+    C = torch.full((M, N), 5.0, dtype=dt, device="cuda")
+    Z = torch.full((M, N), 6.0, dtype=dt, device="cuda")
+    bias = small_ints((groups, N), -9, 9, 1)
+    A, B = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    index, offsets = i32(np.arange(M) % 7), i32(off)
+    with tg.GroupPlan(groups, M, N, 0, code, tg.LAYOUTS[layout], tile_rows=tile) as p:
+        p.run(A.data_ptr(), B.data_ptr(), C.data_ptr(), offsets.data_ptr(),
+              row_index=index.data_ptr() if gather else None, a_rows=7, preact=Z.data_ptr(), bias=bias.data_ptr(),
+              epilogue=tg.GEMM_EPI_BIAS_RELU, stream=stream())
+    want = torch.full_like(Z, 6.0)
+    for g in range(groups):
+        want[off[g]:off[g + 1]] = bias[g].to(dt)
+    inside = (torch.arange(M, device="cuda") >= off[0]) & (torch.arange(M, device="cuda") < off[-1])
+    assert torch.equal(Z, want)
+    assert torch.equal(C, torch.where(inside[:, None], want.clamp(min=0), torch.full_like(C, 5.0)))
+
+
+DENSE = ([(code, lay, k) for code in (BF, F32O) for lay in ("bt", "bt_preshuffled", "bn") for k in ("auto", "tile256")] +
+         [(code, lay, "auto") for code in (BF, F32O) for lay in ("at", "at_bn")] +
+         [(code, lay, "auto") for code in (E4, I8) for lay in ("bt", "bt_preshuffled", "bn", "at", "at_bn")])
+
+
+@pytest.mark.parametrize("code,layout,kernel", DENSE)
+@pytest.mark.parametrize("M", [304, 48])
+def test_product_with_no_inner_size(code, layout, kernel, M):
+    print("case K=0", code, layout, kernel, M, flush=True)
+    N = 528
+    dt = ctype(code)
+    bias = small_ints((N,), -9, 9, 2)
+    R = small_ints((M, N), -64, 64, 3, dt)
+    A, B = torch.zeros(64, device="cuda"), torch.zeros(64, device="cuda")
+    C, C0, Z = torch.full_like(R, 5.0), torch.full_like(R, 5.0), torch.full_like(R, 6.0)
+    with tg.Plan(M, N, 0, code, tg.LAYOUTS[layout], kernel=tg.KERNELS[kernel]) as p:
+        p.run_res(A.data_ptr(), B.data_ptr(), C.data_ptr(), residual=R.data_ptr(), preact=Z.data_ptr(),
+                  bias=bias.data_ptr(), epilogue=tg.GEMM_EPI_BIAS_RELU, stream=stream())
+        p.run_ex(A.data_ptr(), B.data_ptr(), C0.data_ptr(), bias=bias.data_ptr(), epilogue=tg.GEMM_EPI_BIAS_RELU,
+                 stream=stream())
+    z = bias.expand(M, N)
+    assert torch.equal(Z, z.to(dt)) and torch.equal(C0, z.clamp(min=0).to(dt))
+    assert torch.equal(C, (z.clamp(min=0) + R.float()).to(dt))

@@ -39,6 +39,15 @@ __device__ inline __amdgpu_buffer_rsrc_t make_rsrc(const void *base, uint32_t by
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, (int)bytes, 0x00020000);
 }
 
+// Record count of a resource that starts `skip` bytes into an operand of
+// `total` bytes and ends with it: 0 where nothing is left (K = 0, whatever the
+// column).  Wrapped, the count would pass kOobOffset, and the loads that are
+// to return zeros would read far outside the operand.
+__device__ inline uint32_t rest_bytes(size_t total, size_t skip)
+{
+    return total > skip ? (uint32_t)(total - skip) : 0u;
+}
+
 __device__ inline u32x4 buf_load16(__amdgpu_buffer_rsrc_t r, uint32_t voff, uint32_t soff)
 {
     return __builtin_amdgcn_raw_buffer_load_b128(r, voff, soff, 0);

@@ -114,7 +114,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     constexpr int EA = F8 ? 1 : 2;                       // bytes per element of A
     const uint32_t shA = (uint32_t)sk.kt0 * (AKM ? (uint32_t)KN_ROWS * lda : (uint32_t)kTileKBytes);
     const auto rA = AKM ? make_rsrc((const uint8_t *)p.A + (size_t)m0 * EA + shA,
-                                    (uint32_t)((size_t)p.K * lda - (size_t)m0 * EA - shA))
+                                    rest_bytes((size_t)p.K * lda, (size_t)m0 * EA + shA))
                         : make_rsrc((const uint8_t *)p.A + (size_t)m0 * kb + shA, (uint32_t)rows_a * kb - shA);
     // K x N B: the resource starts at column n0 and ends with the matrix, so
     // K-rows past K read zeros; columns past N read neighbouring data or
@@ -123,7 +123,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     constexpr int EB = F8 ? 1 : 2;                       // bytes per element
     const uint32_t shB = (uint32_t)sk.kt0 * (BKN ? (uint32_t)KN_ROWS * ldb : (BPRE ? 2048u : (uint32_t)kTileKBytes));
     const auto rB = BKN ? make_rsrc((const uint8_t *)p.B + (size_t)n0 * EB + shB,
-                                    (uint32_t)((size_t)p.K * ldb - (size_t)n0 * EB - shB))
+                                    rest_bytes((size_t)p.K * ldb, (size_t)n0 * EB + shB))
                         : make_rsrc((const uint8_t *)p.B + (size_t)n0 * kbB + shB, (uint32_t)rows_b * kbB - shB);
     const int nk = sk.nk;
     const uint32_t tail = sk.tail;

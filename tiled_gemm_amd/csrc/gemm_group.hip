@@ -72,7 +72,7 @@ __device__ inline void group_tile(const TiledArgs &p, int tm, int tn, uint8_t *l
     const auto rA = gather ? make_rsrc(p.A, (uint32_t)p.grp.a_rows * kb)
                            : make_rsrc((const uint8_t *)p.A + (AKM ? (size_t)0 : (size_t)m0 * kb),
                                        AKM ? 0u : (uint32_t)rows_a * kb);
-    const auto rB = BKN ? make_rsrc((const uint8_t *)p.B + (size_t)n0 * 2, AKM ? 0u : (uint32_t)((size_t)p.K * ldb - (size_t)n0 * 2))
+    const auto rB = BKN ? make_rsrc((const uint8_t *)p.B + (size_t)n0 * 2, AKM ? 0u : rest_bytes((size_t)p.K * ldb, (size_t)n0 * 2))
                         : make_rsrc((const uint8_t *)p.B + (size_t)n0 * kb, (uint32_t)rows_b * kb);
     uint32_t voffA[AR], voffB[BR];
     uint32_t tailA = 0, tailB = 0;

@@ -98,7 +98,7 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     // rows past K read zeros (columns past N read neighbouring data or zeros
     // and only feed columns of C that are never stored).
     const uint32_t ldb = (uint32_t)p.ldb_bytes;
-    const auto rB = BKN ? make_rsrc((const uint8_t *)p.B + (size_t)n0 * 2, (uint32_t)((size_t)p.K * ldb - (size_t)n0 * 2))
+    const auto rB = BKN ? make_rsrc((const uint8_t *)p.B + (size_t)n0 * 2, rest_bytes((size_t)p.K * ldb, (size_t)n0 * 2))
                         : make_rsrc((const uint8_t *)p.B + (size_t)n0 * kb, (uint32_t)rows_b * kb);
     const int nk = p.k_tiles;
     const uint32_t tail = (uint32_t)p.tail_bytes;
