@@ -448,7 +448,8 @@ typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after cre
  *       matrices M x N.  Every matrix of C is written, zeros for an empty
  *       group:
  *           C_g = cvt( sum over rows r of group g of A[r]^T * B[r] )
- *       K may be any number here; M * 2 % 16 == 0.
+ *       K may be any number here; M * 2 % 16 == 0; M < 2^24 (a step's 64
+ *       rows of A stay inside one 2^31-byte buffer range).
  *   dtype    GEMM_BF16_OUT_F32, GEMM_BF16_OUT_BF16, GEMM_E4M3_OUT_BF16 (the
  *            last with GEMM_LAYOUT_BT and GEMM_LAYOUT_BT_PRESHUFFLED).
  * The other requirements are gemm_plan_create's (N % 16 == 0; K * elem_bytes

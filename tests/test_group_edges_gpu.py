@@ -90,3 +90,20 @@ def test_product_with_no_inner_size(code, layout, kernel, M):
     z = bias.expand(M, N)
     assert torch.equal(Z, z.to(dt)) and torch.equal(C0, z.clamp(min=0).to(dt))
     assert torch.equal(C, (z.clamp(min=0) + R.float()).to(dt))
+
+
+# ------------------------------------------------------------------ the largest rows of a weight gradient
+
+def test_weight_gradient_with_the_longest_rows():
+    """M just below 2^24: the last of a step's 64 K-rows lies 2^31 bytes behind the first."""
+    M, N, rows = (1 << 24) - 8, 16, 70
+    print("case weight gradient, longest rows", M, flush=True)
+    A, B = small_ints((rows, M), -3, 3, 4, torch.bfloat16), small_ints((rows, N), -3, 3, 5, torch.bfloat16)
+    C = torch.empty((2, M, N), dtype=torch.bfloat16, device="cuda")
+    off = i32([0, 3, rows])
+    with tg.GroupPlan(2, M, N, rows, BF, tg.GEMM_LAYOUT_AT_BN) as p:
+        p.run(A.data_ptr(), B.data_ptr(), C.data_ptr(), off.data_ptr(), stream=stream())
+    for cols in (slice(0, 4096), slice(M // 2 - 100, M // 2 + 2000), slice(M - 4000, M)):
+        for g, r in enumerate((slice(0, 3), slice(3, rows))):
+            want = A[r, cols].float().t().contiguous() @ B[r].float()
+            assert torch.equal(C[g, cols], want.to(torch.bfloat16))

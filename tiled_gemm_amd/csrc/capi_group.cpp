@@ -25,6 +25,7 @@ namespace {
 
 constexpr int64_t kMaxRows = GEMM_GROUP_MAX_ROWS;
 constexpr int64_t kRange = (int64_t)1 << 31;     // bytes one buffer resource of the kernels covers
+constexpr int64_t kStepRows = 64;                // K-rows of one step with a ragged inner size (bf16)
 
 const tg::GroupVariant *find(const tg::GroupVariant *v, int n, int bm, int elem, int out, int layout)
 {
@@ -99,6 +100,10 @@ gemm_group_plan *gemm_group_plan_create_opt(int groups, int64_t M, int64_t N, in
     }
     if ((inner ? K : M) > kMaxRows) {
         capi_fail(GEMM_ERR_UNSUPPORTED, "more than 2^24 grouped rows");
+        return nullptr;
+    }
+    if (inner && M * kStepRows * (int64_t)sizeof(uint16_t) >= kRange) {
+        capi_fail(GEMM_ERR_UNSUPPORTED, "M=%lld: 64 rows of A must stay below 2^31 bytes (32-bit offsets)", (long long)M);
         return nullptr;
     }
     // One group's product: gemm_plan_create's checks on the sizes.  The
