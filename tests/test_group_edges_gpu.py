@@ -107,3 +107,46 @@ def test_weight_gradient_with_the_longest_rows():
         for g, r in enumerate((slice(0, 3), slice(3, rows))):
             want = A[r, cols].float().t().contiguous() @ B[r].float()
             assert torch.equal(C[g, cols], want.to(torch.bfloat16))
+
+
+# ------------------------------------------------------------------ the most tokens
+
+def test_combine_and_gradient_of_the_most_tokens():
+    """2^24 tokens: workgroups of 256 threads for each would be 2^32 threads."""
+    T, N = tg.GEMM_GROUP_MAX_ROWS, 16
+    print("case most tokens", T, flush=True)
+    src, dout = small_ints((T, N), -3, 3, 6, torch.bfloat16), small_ints((T, N), -3, 3, 7, torch.bfloat16)
+    row = torch.randperm(T, device="cuda").to(torch.int32)
+    row[::1001] = -1
+    w = torch.full((T,), 2.0, device="cuda")
+    out, dsrc = torch.full_like(src, 5.0), torch.full_like(src, 5.0)
+    dw = torch.full((T,), 5.0, device="cuda")
+    tg.gemm_group_combine(T, 1, N, tg.GEMM_TYPE_BF16, src.data_ptr(), T, row.data_ptr(), out.data_ptr(),
+                          weights=w.data_ptr(), stream=stream())
+    tg.gemm_group_combine_grad(T, 1, N, tg.GEMM_TYPE_BF16, dout.data_ptr(), src.data_ptr(), T, row.data_ptr(),
+                               w.data_ptr(), dsrc.data_ptr(), dw.data_ptr(), stream())
+    live = row >= 0
+    at = row.clamp(min=0).long()
+    assert torch.equal(out, torch.where(live[:, None], 2 * src[at], 0))
+    want = torch.full_like(src, 5.0)
+    want[at[live]] = 2 * dout[live]
+    assert torch.equal(dsrc, want)
+    assert torch.equal(dw, (src[at].float() * dout.float()).sum(1) * live)
+
+
+def test_combine_past_the_largest_grid():
+    """64 GiB of output: a workgroup for every 256 items of 8 columns would be 2^32 threads."""
+    T, N = tg.GEMM_GROUP_MAX_ROWS, 2048
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of device memory")
+    print("case largest grid of combine", T, N, flush=True)
+    src = small_ints((997, N), -3, 3, 8, torch.bfloat16)
+    row = (torch.arange(T, device="cuda") % 1000).to(torch.int32)       # 997, 998, 999: rows that src does not have
+    out = torch.empty((T, N), dtype=torch.bfloat16, device="cuda")
+    tg.gemm_group_combine(T, 1, N, tg.GEMM_TYPE_BF16, src.data_ptr(), 997, row.data_ptr(), out.data_ptr(), stream=stream())
+    table = torch.cat([src, torch.zeros((3, N), dtype=torch.bfloat16, device="cuda")])
+    for lo in (0, 1 << 20, (1 << 23) - 5000, (1 << 23) + 77, T - 8000):
+        at = torch.arange(lo, lo + 8000, device="cuda")
+        assert torch.equal(out[lo:lo + 8000], table[at % 1000])
+    del out
+    torch.cuda.empty_cache()

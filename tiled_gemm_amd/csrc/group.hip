@@ -198,6 +198,8 @@ __device__ inline void store8(void *base, size_t at, const float (&v)[8])
 }
 
 constexpr int kCombineThreads = 256;
+// A launch has fewer than 2^32 threads.
+constexpr int64_t kCombineBlocks = (int64_t)1 << 23;
 
 }  // namespace
 
@@ -240,7 +242,7 @@ __global__ __launch_bounds__(kCombineThreads) void group_combine_kernel(const Co
 hipError_t launch_group_combine(const CombineArgs &a, hipStream_t s)
 {
     const int64_t blocks = (a.tokens * (a.N / 8) + kCombineThreads - 1) / kCombineThreads;
-    const unsigned grid = (unsigned)(blocks < (1 << 24) ? blocks : (1 << 24));
+    const unsigned grid = (unsigned)(blocks < kCombineBlocks ? blocks : kCombineBlocks);
     if (a.type == kOutF32)
         hipLaunchKernelGGL(group_combine_kernel<kOutF32>, dim3(grid), dim3(kCombineThreads), 0, s, a);
     else
@@ -316,14 +318,31 @@ __global__ __launch_bounds__(kCombineThreads) void group_combine_grad_kernel(con
     }
 }
 
-hipError_t launch_group_combine_grad(const CombineArgs &a, hipStream_t s)
+// One workgroup per token, the tokens in as many launches as their number needs
+// (one up to 2^23).
+hipError_t launch_group_combine_grad(const CombineArgs &args, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.tokens), threads(kCombineThreads);
-    if (a.type == kOutF32)
-        hipLaunchKernelGGL(group_combine_grad_kernel<kOutF32>, grid, threads, 0, s, a);
-    else
-        hipLaunchKernelGGL(group_combine_grad_kernel<kOutBf16>, grid, threads, 0, s, a);
-    return hipGetLastError();
+    const dim3 threads(kCombineThreads);
+    const int64_t bytes = args.type == kOutF32 ? 4 : 2;
+    for (int64_t first = 0; first < args.tokens; first += kCombineBlocks) {
+        CombineArgs a = args;
+        a.tokens = args.tokens - first < kCombineBlocks ? args.tokens - first : kCombineBlocks;
+        a.d_out = (const uint8_t *)args.d_out + first * args.N * bytes;
+        a.slot_row += first * args.topk;
+        if (a.weights)
+            a.weights += first * args.topk;
+        if (a.d_weights)
+            a.d_weights += first * args.topk;
+        const dim3 grid((unsigned)a.tokens);
+        if (a.type == kOutF32)
+            hipLaunchKernelGGL(group_combine_grad_kernel<kOutF32>, grid, threads, 0, s, a);
+        else
+            hipLaunchKernelGGL(group_combine_grad_kernel<kOutBf16>, grid, threads, 0, s, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 // ---------------------------------------------------------------------------
