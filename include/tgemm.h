@@ -454,7 +454,8 @@ typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after cre
  *            last with GEMM_LAYOUT_BT and GEMM_LAYOUT_BT_PRESHUFFLED).
  * The other requirements are gemm_plan_create's (N % 16 == 0; K * elem_bytes
  * % 64 == 0 where rows are grouped; ...); grouped rows at most
- * GEMM_GROUP_MAX_ROWS.  Host only.  NULL on error; freed with
+ * GEMM_GROUP_MAX_ROWS; all tiles of one launch together fewer than 2^32
+ * threads (gemm_group_plan_info: grid * threads).  Host only.  NULL on error; freed with
  * gemm_group_plan_destroy.
  */
 gemm_group_plan *gemm_group_plan_create(int groups, int64_t M, int64_t N, int64_t K, int dtype, int layout);

@@ -25,6 +25,7 @@ namespace {
 
 constexpr int64_t kMaxRows = GEMM_GROUP_MAX_ROWS;
 constexpr int64_t kRange = (int64_t)1 << 31;     // bytes one buffer resource of the kernels covers
+constexpr int64_t kThreads = (int64_t)1 << 32;   // a launch has fewer
 constexpr int64_t kStepRows = 64;                // K-rows of one step with a ragged inner size (bf16)
 
 const tg::GroupVariant *find(const tg::GroupVariant *v, int n, int bm, int elem, int out, int layout)
@@ -155,9 +156,9 @@ gemm_group_plan *gemm_group_plan_create_opt(int groups, int64_t M, int64_t N, in
     p->group_m = bm >= 256 ? 4 : 8;
     if (inner && p->group_m > p->tiles_m)
         p->group_m = p->tiles_m > 0 ? p->tiles_m : 1;
-    if (tiles * p->tiles_n >= kRange) {
+    if (tiles * p->tiles_n * p->v->threads >= kThreads) {
         gemm_group_plan_destroy(p);
-        capi_fail(GEMM_ERR_UNSUPPORTED, "too many tiles");
+        capi_fail(GEMM_ERR_UNSUPPORTED, "too many tiles (a launch has fewer than 2^32 threads)");
         return nullptr;
     }
     I.grid = (int32_t)(tiles * p->tiles_n);
