@@ -290,9 +290,12 @@ int gemm_run_ws(const gemm_plan *plan, const void *A, const void *B, void *C,
  *             gemm_act_grad takes it for the backward pass.
  *   workspace, workspace_bytes  as for gemm_run_ws (NULL, 0: no split).  It
  *             must not overlap the residual either.
- * Plans with GEMM_KERNEL_AUTO or GEMM_KERNEL_TILE256; the other explicit
- * kernel choices give GEMM_ERR_UNSUPPORTED when a residual or preact is
- * given.  With neither, the call is gemm_run_ws.  Errors as gemm_run_ws.
+ * Every plan with GEMM_KERNEL_AUTO, GEMM_KERNEL_TILE256 or
+ * GEMM_KERNEL_GENERIC_128, and GEMM_KERNEL_PIPE with a pre-shuffled B or
+ * W4A8, has this epilogue; GEMM_KERNEL_GENERIC_256, GEMM_KERNEL_PIPE4 and
+ * GEMM_KERNEL_PIPE otherwise give GEMM_ERR_UNSUPPORTED when a residual or
+ * preact is given.  With neither, the call is gemm_run_ws.  Errors as
+ * gemm_run_ws.
  */
 int gemm_run_res(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
                  const void *residual, void *preact, void *workspace, size_t workspace_bytes, hipStream_t stream);

@@ -941,8 +941,8 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
         return fail(GEMM_ERR_INVALID_ARG, "preact overlaps A, B, C or the residual");
     if ((residual || preact) &&
         (I.kernel == 1 ? plan->skinny->launch_ex == nullptr : plan->ex_v == nullptr))
-        return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no residual epilogue (GEMM_KERNEL_AUTO and "
-                                          "GEMM_KERNEL_TILE256 have)");
+        return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no residual epilogue (GEMM_KERNEL_AUTO, "
+                                          "GEMM_KERNEL_TILE256 and GEMM_KERNEL_GENERIC_128 have)");
     e->res = residual;
     e->pre = preact;
     return GEMM_OK;
