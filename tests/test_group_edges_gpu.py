@@ -150,3 +150,23 @@ def test_combine_past_the_largest_grid():
         assert torch.equal(out[lo:lo + 8000], table[at % 1000])
     del out
     torch.cuda.empty_cache()
+
+
+# ------------------------------------------------------------------ no rows at all
+
+@pytest.mark.parametrize("code", [BF, F32O])
+def test_weight_gradient_without_room_for_rows(code):
+    print("case weight gradient, K = 0", code, flush=True)
+    A, off = torch.zeros(64, device="cuda"), i32([0, 0, 0, 0])
+    C = torch.full((3, 264, 528), 9.0, dtype=ctype(code), device="cuda")
+    with tg.GroupPlan(3, 264, 528, 0, code, tg.GEMM_LAYOUT_AT_BN) as p:
+        p.run(A.data_ptr(), A.data_ptr(), C.data_ptr(), off.data_ptr(), stream=stream())
+    assert not C.any()
+
+
+@pytest.mark.parametrize("groups", [1, 3])
+def test_bias_gradient_of_no_rows(groups):
+    db, off = torch.full((groups, 272), 4.0, device="cuda"), i32([0] * (groups + 1))
+    tg.gemm_act_grad(0, 272, tg.GEMM_TYPE_BF16, tg.GEMM_EPI_BIAS_SILU, 0, None, 0, db.data_ptr(), groups=groups,
+                     offsets=off.data_ptr() if groups > 1 else None, stream=stream())
+    assert not db.any()
