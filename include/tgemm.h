@@ -7,7 +7,8 @@
  *
  *     C[m][n] = cvt( (sum_k A[m][k] * B[n][k]) * s_a * s_b )
  *
- * products of the input elements summed in fp32, the scale applied in fp32
+ * products of the input elements summed in fp32 (fp8: by the matrix unit, in
+ * fewer bits; see GEMM_E4M3_OUT_BF16), the scale applied in fp32
  * as (acc * s_a) * s_b (the Kernel Authoring skill's section 3 shows that
  * order), then converted to the output type with round-to-nearest-even.
  *
@@ -72,7 +73,14 @@ typedef enum {
 typedef enum {
     GEMM_BF16_OUT_F32 = 0,       /* A, B bf16; C fp32 (no rounding of the fp32 sum)   */
     GEMM_BF16_OUT_BF16 = 1,      /* A, B bf16; C bf16                                 */
-    GEMM_E4M3_OUT_BF16 = 2,      /* A, B OCP fp8 e4m3fn (max 448); C bf16             */
+    GEMM_E4M3_OUT_BF16 = 2,      /* A, B OCP fp8 e4m3fn (max 448); C bf16.  The matrix
+                                    unit (also for MXFP8) adds 8 products along K at a
+                                    time and drops what lies more than 13 binary places
+                                    below the largest; the sums of 8 are added in fp32.
+                                    Measured on N(0, 1) data against sum |a b|: at most
+                                    2.1e-5 at K = 128, 3.1e-6 at 2048, 1.0e-6 at 8192.
+                                    (e4m3 converts to bf16 exactly: a bf16 plan keeps fp32
+                                    sums, at half the rate.)                          */
     GEMM_MXFP8_OUT_BF16 = 3,     /* A, B MX: e4m3fn elements + E8M0 scales; C bf16    */
     GEMM_MXFP4_OUT_BF16 = 4,     /* A, B MX: e2m1 elements (2 per byte) + E8M0; C bf16 */
     GEMM_I8_OUT_BF16 = 5,        /* A, B int8, exact int32 sums; C bf16               */
@@ -290,6 +298,11 @@ int gemm_run_ws(const gemm_plan *plan, const void *A, const void *B, void *C,
  *             gemm_act_grad takes it for the backward pass.
  *   workspace, workspace_bytes  as for gemm_run_ws (NULL, 0: no split).  It
  *             must not overlap the residual either.
+ * SiLU: the tiled bf16, fp8 and integer kernels evaluate it with the hardware's
+ * 2^x and reciprocal, the skinny ones, the split-K reduction, MX plans and the
+ * transposed 8-bit layouts with expf and a division.  Both stay within
+ * 2^-20 |z|, but the last bit of C may depend on the kernel, and so on M and
+ * on whether a workspace is given (as the order of the sums does).
  * Every plan with GEMM_KERNEL_AUTO, GEMM_KERNEL_TILE256 or
  * GEMM_KERNEL_GENERIC_128, and GEMM_KERNEL_PIPE with a pre-shuffled B or
  * W4A8, has this epilogue; GEMM_KERNEL_GENERIC_256, GEMM_KERNEL_PIPE4 and
@@ -425,7 +438,9 @@ int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, 
  *
  * and backwards gemm_group_combine_grad, gemm_act_grad, gemm_group_run with
  * GEMM_LAYOUT_BN (input gradients) and GEMM_LAYOUT_AT_BN (weight gradients),
- * and gemm_group_combine without weights (the gradient of the gather).
+ * and gemm_group_combine without weights (the gradient of the gather).  The
+ * weight gradient has no row_index: for the up projection the caller gathers
+ * the tokens' rows (row_token) into an array of their own first.
  * ------------------------------------------------------------------------ */
 #define GEMM_GROUP_MAX 1024                 /* most groups                            */
 #define GEMM_GROUP_MAX_ROWS ((int64_t)1 << 24)   /* most rows (or slots) of one call */
@@ -598,7 +613,8 @@ int gemm_group_combine_grad(int64_t tokens, int topk, int64_t N, int type, const
  *              then 1).  Rows outside every group: d_z is left as it was.
  *   workspace  gemm_act_grad_workspace_bytes(M, N, groups) bytes when d_bias is
  *              given (16-byte aligned, contents undefined before and after);
- *              not read otherwise.
+ *              not read otherwise.  Calls that share one must not overlap in
+ *              time.
  * d_bias is summed in a fixed order (no atomics): the same on every run.
  * Asynchronous; allocates nothing.  GEMM_OK or an error.
  */

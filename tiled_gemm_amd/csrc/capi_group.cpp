@@ -54,6 +54,12 @@ const tg::GroupVariant *pick(int bm, int elem, int out, int layout)
 // 48: 60 / 55 / 61 / 66; mean 120: 106 / 85 / 81 / 83; 16 groups, N 2048, K 4096:
 // mean 80: 74 / 59 / 70 / 94; mean 170: 121 / 100 / 76 / 103; mean 300 (64 / 128 /
 // 256): 147 / 139 / 115; mean 1000: 392 / 319 / 291.
+// One list serves all types and layouts; where it is not the best of the four
+// (16 groups, N 2048, K 4096): e4m3 mean 400 (64 / 128 / 256) 77 / 61 / 67, mean 600
+// 107 / 89 / 100; bf16 pre-shuffled mean 24 (32 / 64) 57 / 44.  The rule does not
+// look at the number of workgroups: few groups with N below 1024, not
+// measured, leave CUs idle, as the weight gradient's 256 x 256 tiles do where
+// the groups' C are small.
 int default_tile(int groups, int64_t M, int layout)
 {
     if (layout == GEMM_LAYOUT_AT_BN)
