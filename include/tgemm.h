@@ -222,7 +222,8 @@ typedef struct {
                                     aligned when per column                                      */
     const float *bias;           /* device; N values, 16-byte aligned; required by the bias
                                     epilogues, NULL for GEMM_EPI_NONE                             */
-    int32_t scale_a_per_row;     /* 0: scale_a[0] scales every row; 1: scale_a[m] scales row m    */
+    int32_t scale_a_per_row;     /* 0: scale_a[0] scales every row; 1: scale_a[m] scales row m
+                                    (M below 2^30)                                                */
     int32_t scale_b_per_col;     /* 0: scale_b[0] scales every column; 1: scale_b[n] column n     */
     int32_t epilogue;            /* gemm_epilogue                                                 */
 } gemm_epilogue_args;
@@ -473,8 +474,8 @@ typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after cre
  * The other requirements are gemm_plan_create's (N % 16 == 0; K * elem_bytes
  * % 64 == 0 where rows are grouped; ...); grouped rows at most
  * GEMM_GROUP_MAX_ROWS; all tiles of one launch together fewer than 2^32
- * threads (gemm_group_plan_info: grid * threads).  Host only.  NULL on error; freed with
- * gemm_group_plan_destroy.
+ * threads (gemm_group_plan_info: grid * threads).  Host only.  NULL on error;
+ * freed with gemm_group_plan_destroy.
  */
 gemm_group_plan *gemm_group_plan_create(int groups, int64_t M, int64_t N, int64_t K, int dtype, int layout);
 

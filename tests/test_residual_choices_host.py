@@ -40,3 +40,15 @@ def test_choices_with_a_residual_epilogue(kernel, kw):
             assert "NULL A" in why(p, code)                  # neither: gemm_run_ws
             seen += 1
     assert seen
+
+
+@pytest.mark.parametrize("per_row,why", [(True, "below 2\\^30"), (False, "NULL A")])
+def test_a_scale_per_row_of_the_most_rows(per_row, why):
+    """2^30 scales are 2^32 bytes: their record count in 32 bits would be 0."""
+    with tg.Plan(1 << 30, 16, 32, tg.GEMM_BF16_OUT_BF16, tg.GEMM_LAYOUT_BT) as p:
+        for call in (lambda **kw: p.run_ex(0, Q, R, **kw), lambda **kw: p.run_res(0, Q, R, residual=R, **kw)):
+            with pytest.raises(tg.GemmError, match=why):
+                call(scale_a=S, scale_a_per_row=per_row)
+    with tg.Plan((1 << 30) - 1, 16, 32, tg.GEMM_BF16_OUT_BF16, tg.GEMM_LAYOUT_BT) as p:
+        with pytest.raises(tg.GemmError, match="NULL A"):
+            p.run_ex(0, Q, R, scale_a=S, scale_a_per_row=True)

@@ -754,6 +754,8 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         ok();
         return GEMM_OK;
     }
+    if (epi.sa && epi.sa_rows && I.M >= kMaxDim)
+        return fail(GEMM_ERR_UNSUPPORTED, "a scale per row needs M below 2^30 (32-bit offsets)");
     if (!A && I.K)
         return fail(GEMM_ERR_INVALID_ARG, "NULL A");
     if (!B && I.K)

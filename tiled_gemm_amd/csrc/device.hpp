@@ -532,12 +532,11 @@ __device__ inline void epi_finish4(const EpiView &v, const EpiExt &x, __amdgpu_b
 template <int FN, int BATCH>
 constexpr int epi_lds_floats() { return BATCH * 16 * (16 * FN + 4); }    // per wave
 
-// (epi_finish4 and epi_finish2, the epilogues of the skinny kernels, the MX and
-// the transposed 8-bit layouts, keep epi_act's expf and division.)
 // SiLU with the hardware's exponential and reciprocal (each within an ulp or
 // so): z / (1 + 2^(-z log2 e)).  The error of the exponent's argument is at most
 // |z| 2^-23 relative to e^-z, far below the epilogue's 2^-20 |z|; the limits at
-// the infinities are those of the division.
+// the infinities are those of the division.  (epi_finish4 and epi_finish2 keep
+// epi_act's expf and division.)
 __device__ inline float epi_silu(float z)
 {
     return z * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
