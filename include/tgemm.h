@@ -624,6 +624,52 @@ int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c,
                   float *d_bias, int groups, const int32_t *offsets, void *workspace, size_t workspace_bytes,
                   hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Activations kept in 8 bits between the forward and the backward pass.  Of a
+ * row's every 32 columns (the last block of a row may have 16) the checkpoint
+ * holds e4m3 elements and one power of two:
+ *
+ *   s[m][b] = the smallest power of two, 2^-127 or more, with |x| <= 448 s for every finite x of the block
+ *   q[m][n] = e4m3( x[m][n] / s )        (nearest even; no element is clipped; Inf and NaN become NaN)
+ *   value   = q[m][n] * s[m][n / 32]
+ *
+ *   q       M x N bytes row-major, 16-byte aligned;
+ *   scales  M x ceil(N / 32) bytes row-major, E8M0: s = 2^(byte - 127), 255 NaN.
+ * 33 / 32 bytes per element instead of 2 or 4, each within 2^-4 of itself (and
+ * within 2^-10 s near zero).  With N a multiple of 64 the pair is an operand of
+ * the MXFP8 products (q as A or B, scales through gemm_preshuffle_bscale).
+ *
+ * The usual use: gemm_run_res or gemm_group_run saves the pre-activation z,
+ * gemm_ckpt_pack keeps it; backwards gemm_act_grad_ckpt makes d_z from it, and
+ * gemm_ckpt_unpack with the activation makes the layer's output again, the
+ * operand of the next layer's weight gradient (GEMM_LAYOUT_AT_BN).
+ *   M, N    rows and columns: 0 .. GEMM_GROUP_MAX_ROWS; N % 16 == 0, N < 2^21.
+ *   type    gemm_type of src, out, d_c and d_z (GEMM_TYPE_F32 or GEMM_TYPE_BF16).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * gemm_ckpt_pack -- src (M x N, 16-byte aligned) into q and scales.  None of
+ * the three overlap.  Asynchronous; one launch; GEMM_OK or an error.
+ */
+int gemm_ckpt_pack(int64_t M, int64_t N, int type, const void *src, void *q, void *scales, hipStream_t stream);
+
+/*
+ * gemm_ckpt_unpack -- out[m][n] = cvt( act(value) ), act the activation of
+ * `epilogue` (a gemm_epilogue; NONE and BIAS: none).  out is 16-byte aligned and
+ * overlaps neither q nor scales.  Asynchronous; one launch; GEMM_OK or an error.
+ */
+int gemm_ckpt_unpack(int64_t M, int64_t N, int type, int epilogue, const void *q, const void *scales, void *out,
+                     hipStream_t stream);
+
+/*
+ * gemm_act_grad_ckpt -- gemm_act_grad with z read from its checkpoint (q and
+ * scales may be NULL without an activation).  d_z may be d_c, and overlaps
+ * neither q nor scales.  The workspace is gemm_act_grad_workspace_bytes.
+ */
+int gemm_act_grad_ckpt(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *q,
+                       const void *scales, void *d_z, float *d_bias, int groups, const int32_t *offsets,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* gemm_last_error -- message for the calling thread's last failure ("" if none). */
 const char *gemm_last_error(void);
 

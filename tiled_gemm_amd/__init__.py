@@ -58,7 +58,7 @@ EXPORTS = (
     "gemm_group_plan_create", "gemm_group_plan_create_opt", "gemm_group_plan_destroy", "gemm_group_plan_query",
     "gemm_group_preshuffled_b_bytes", "gemm_group_preshuffle_b", "gemm_group_run", "gemm_group_sort_workspace_bytes",
     "gemm_group_sort", "gemm_group_combine", "gemm_group_combine_grad", "gemm_act_grad_workspace_bytes",
-    "gemm_act_grad",
+    "gemm_act_grad", "gemm_ckpt_pack", "gemm_ckpt_unpack", "gemm_act_grad_ckpt",
 )
 
 GEMM_STATIC_WORKSPACE_BYTES = 64 << 20
@@ -148,6 +148,9 @@ def load() -> ctypes.CDLL:
         "gemm_group_combine_grad": (c_int, [i64, c_int, i64, c_int, vp, vp, i64, vp, vp, vp, vp, vp]),
         "gemm_act_grad_workspace_bytes": (ctypes.c_size_t, [i64, i64, c_int]),
         "gemm_act_grad": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp, c_int, vp, vp, ctypes.c_size_t, vp]),
+        "gemm_ckpt_pack": (c_int, [i64, i64, c_int, vp, vp, vp, vp]),
+        "gemm_ckpt_unpack": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp]),
+        "gemm_act_grad_ckpt": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp, vp, c_int, vp, vp, ctypes.c_size_t, vp]),
         "gemm_last_error": (ctypes.c_char_p, []),
         "gemm_plan_query": (c_int, [vp, ctypes.POINTER(gemm_plan_info)]),
         "gemm_plan_layout": (c_int, [vp, c_int, p32, p64, p64]),
@@ -354,6 +357,23 @@ def gemm_act_grad(M: int, N: int, type: int, epilogue: int, d_c: int, z: int | N
                   workspace: int | None = None, workspace_bytes: int = 0, stream: int = 0) -> None:
     _check(load().gemm_act_grad(M, N, type, epilogue, d_c, z or None, d_z, d_bias or None, groups, offsets or None,
                                 workspace or None, workspace_bytes, stream), "gemm_act_grad")
+
+
+def gemm_ckpt_pack(M: int, N: int, type: int, src: int, q: int, scales: int, stream: int = 0) -> None:
+    _check(load().gemm_ckpt_pack(M, N, type, src, q, scales, stream), "gemm_ckpt_pack")
+
+
+def gemm_ckpt_unpack(M: int, N: int, type: int, epilogue: int, q: int, scales: int, out: int,
+                     stream: int = 0) -> None:
+    _check(load().gemm_ckpt_unpack(M, N, type, epilogue, q, scales, out, stream), "gemm_ckpt_unpack")
+
+
+def gemm_act_grad_ckpt(M: int, N: int, type: int, epilogue: int, d_c: int, q: int | None, scales: int | None,
+                       d_z: int, d_bias: int | None = None, groups: int = 1, offsets: int | None = None,
+                       workspace: int | None = None, workspace_bytes: int = 0, stream: int = 0) -> None:
+    _check(load().gemm_act_grad_ckpt(M, N, type, epilogue, d_c, q or None, scales or None, d_z, d_bias or None,
+                                     groups, offsets or None, workspace or None, workspace_bytes, stream),
+           "gemm_act_grad_ckpt")
 
 
 def gemm_plan_query(plan: int) -> dict:

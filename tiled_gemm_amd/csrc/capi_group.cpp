@@ -504,9 +504,18 @@ size_t gemm_act_grad_workspace_bytes(int64_t M, int64_t N, int groups)
     return (size_t)act_chunks(M, N, groups) * (size_t)N * 4;
 }
 
-int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *z, void *d_z,
-                  float *d_bias, int groups, const int32_t *offsets, void *workspace, size_t workspace_bytes,
-                  hipStream_t stream)
+namespace {
+
+int act_of(int epilogue)
+{
+    static const int kAct[] = {tg::kActNone, tg::kActNone, tg::kActRelu, tg::kActSilu, tg::kActGelu};
+    return kAct[epilogue];
+}
+
+// z: M x N of the type, or (checkpointed) its e4m3 elements with their scales.
+int act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *z, bool checkpointed,
+             const void *scales, void *d_z, float *d_bias, int groups, const int32_t *offsets, void *workspace,
+             size_t workspace_bytes, hipStream_t stream)
 {
     if (groups < 1 || groups > GEMM_GROUP_MAX || (!offsets && groups != 1))
         return capi_fail(GEMM_ERR_INVALID_ARG, "groups=%d outside 1..%d, or several groups without offsets", groups,
@@ -522,33 +531,42 @@ int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c,
         return capi_fail(GEMM_ERR_INVALID_ARG, "unknown epilogue %d", epilogue);
     if (N == 0 || (M == 0 && !d_bias))
         return capi_ok();
-    static const int kAct[] = {tg::kActNone, tg::kActNone, tg::kActRelu, tg::kActSilu, tg::kActGelu};
-    const int act = kAct[epilogue];
+    const int act = act_of(epilogue);
     if (M && (!d_c || !d_z || (!z && act != tg::kActNone)))
         return capi_fail(GEMM_ERR_INVALID_ARG, "NULL d_c, z or d_z");
+    if (M && checkpointed && !scales && act != tg::kActNone)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "NULL scales");
     if (!capi_aligned(d_c, 16) || !capi_aligned(z, 16) || !capi_aligned(d_z, 16) || !capi_aligned(d_bias, 16) ||
         !capi_aligned(offsets, 4))
         return capi_fail(GEMM_ERR_INVALID_ARG, "d_c, z, d_z and d_bias must be 16-byte aligned, offsets 4");
     const size_t bytes = (size_t)M * (size_t)N * type_bytes(type);
     const size_t bbytes = (size_t)groups * (size_t)N * 4, gbytes = ((size_t)groups + 1) * 4;
-    if ((d_z != d_c && capi_overlap(d_z, bytes, d_c, bytes)) || (d_z != z && capi_overlap(d_z, bytes, z, bytes)))
-        return capi_fail(GEMM_ERR_INVALID_ARG, "d_z must be d_c or z itself, or overlap neither");
+    const int64_t blocks = (N + 31) / 32;
+    const size_t zbytes = checkpointed ? (size_t)M * (size_t)N : bytes;
+    const size_t xbytes = checkpointed ? (size_t)M * (size_t)blocks : 0;
+    if ((d_z != d_c && capi_overlap(d_z, bytes, d_c, bytes)) ||
+        ((checkpointed || d_z != z) && capi_overlap(d_z, bytes, z, zbytes)))
+        return capi_fail(GEMM_ERR_INVALID_ARG, checkpointed ? "d_z must be d_c itself, or overlap neither d_c nor q"
+                                                            : "d_z must be d_c or z itself, or overlap neither");
     if (capi_overlap(d_z, bytes, offsets, gbytes) || capi_overlap(d_bias, bbytes, d_z, bytes) ||
-        capi_overlap(d_bias, bbytes, d_c, bytes) || capi_overlap(d_bias, bbytes, z, bytes) ||
-        capi_overlap(d_bias, bbytes, offsets, gbytes))
+        capi_overlap(d_bias, bbytes, d_c, bytes) || capi_overlap(d_bias, bbytes, z, zbytes) ||
+        capi_overlap(d_bias, bbytes, offsets, gbytes) || capi_overlap(scales, xbytes, d_z, bytes) ||
+        capi_overlap(scales, xbytes, d_bias, bbytes))
         return capi_fail(GEMM_ERR_INVALID_ARG, "d_bias or the offsets overlap another operand");
     const size_t need = d_bias ? gemm_act_grad_workspace_bytes(M, N, groups) : 0;
     if (need && (!workspace || workspace_bytes < need || !capi_aligned(workspace, 16)))
         return capi_fail(GEMM_ERR_INVALID_ARG, "d_bias needs a 16-byte aligned workspace of %zu bytes", need);
     if (need && (capi_overlap(workspace, need, d_z, bytes) || capi_overlap(workspace, need, d_c, bytes) ||
-                 capi_overlap(workspace, need, z, bytes) || capi_overlap(workspace, need, d_bias, bbytes) ||
-                 capi_overlap(workspace, need, offsets, gbytes)))
+                 capi_overlap(workspace, need, z, zbytes) || capi_overlap(workspace, need, d_bias, bbytes) ||
+                 capi_overlap(workspace, need, offsets, gbytes) || capi_overlap(workspace, need, scales, xbytes)))
         return capi_fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps another operand");
     if (int rc = tg::capi_check_device())
         return rc;
     tg::ActGradArgs a{};
     a.d_c = d_c;
     a.z = z;
+    a.scales = checkpointed ? (const uint8_t *)scales : nullptr;
+    a.blocks = blocks;
     a.d_z = d_z;
     a.d_bias = d_bias;
     a.partial = d_bias ? (float *)workspace : nullptr;
@@ -564,6 +582,96 @@ int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c,
     if (e != hipSuccess)
         return capi_fail(GEMM_ERR_HIP, "epilogue gradient launch: %s", hipGetErrorString(e));
     return capi_ok();
+}
+
+}  // namespace
+
+int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *z, void *d_z,
+                  float *d_bias, int groups, const int32_t *offsets, void *workspace, size_t workspace_bytes,
+                  hipStream_t stream)
+{
+    return act_grad(M, N, type, epilogue, d_c, z, false, nullptr, d_z, d_bias, groups, offsets, workspace,
+                    workspace_bytes, stream);
+}
+
+int gemm_act_grad_ckpt(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *q,
+                       const void *scales, void *d_z, float *d_bias, int groups, const int32_t *offsets,
+                       void *workspace, size_t workspace_bytes, hipStream_t stream)
+{
+    return act_grad(M, N, type, epilogue, d_c, q, true, scales, d_z, d_bias, groups, offsets, workspace,
+                    workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- 8-bit checkpoints
+
+namespace {
+
+int check_ckpt(int64_t M, int64_t N, int type)
+{
+    if (M < 0 || N < 0)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "negative size (M=%lld N=%lld)", (long long)M, (long long)N);
+    if (M > kMaxRows || N >= ((int64_t)1 << 21) || N % 16 != 0)
+        return capi_fail(GEMM_ERR_UNSUPPORTED, "M=%lld must be at most 2^24, N=%lld a multiple of 16 below 2^21",
+                         (long long)M, (long long)N);
+    if (type != GEMM_TYPE_F32 && type != GEMM_TYPE_BF16)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "unknown type %d", type);
+    if (tg::ckpt_units(M, N) >= ((int64_t)1 << 31))
+        return capi_fail(GEMM_ERR_UNSUPPORTED, "M x N is too large for one launch");
+    return GEMM_OK;
+}
+
+// wide: src or out, M x N of the type.
+int run_ckpt(bool pack, int64_t M, int64_t N, int type, int act, const void *wide, const void *q, const void *scales,
+             hipStream_t stream)
+{
+    const char *const name = pack ? "src" : "out";
+    if (M == 0 || N == 0)
+        return capi_ok();
+    if (!wide || !q || !scales)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "NULL %s, q or scales", name);
+    if (!capi_aligned(wide, 16) || !capi_aligned(q, 16))
+        return capi_fail(GEMM_ERR_INVALID_ARG, "%s and q must be 16-byte aligned", name);
+    const int64_t blocks = (N + 31) / 32;
+    const size_t n = (size_t)M * (size_t)N, w = n * type_bytes(type), x = (size_t)M * (size_t)blocks;
+    if (capi_overlap(wide, w, q, n) || capi_overlap(wide, w, scales, x) || capi_overlap(q, n, scales, x))
+        return capi_fail(GEMM_ERR_INVALID_ARG, "%s, q and scales must not overlap", name);
+    if (int rc = tg::capi_check_device())
+        return rc;
+    tg::CkptArgs a{};
+    if (pack)
+        a.src = wide;
+    else
+        a.out = const_cast<void *>(wide);
+    a.q = (uint8_t *)const_cast<void *>(q);
+    a.scales = (uint8_t *)const_cast<void *>(scales);
+    a.M = M;
+    a.N = N;
+    a.blocks = blocks;
+    a.act = act;
+    a.type = out_type(type);
+    const hipError_t e = pack ? tg::launch_ckpt_pack(a, stream) : tg::launch_ckpt_unpack(a, stream);
+    if (e != hipSuccess)
+        return capi_fail(GEMM_ERR_HIP, "checkpoint launch: %s", hipGetErrorString(e));
+    return capi_ok();
+}
+
+}  // namespace
+
+int gemm_ckpt_pack(int64_t M, int64_t N, int type, const void *src, void *q, void *scales, hipStream_t stream)
+{
+    if (int rc = check_ckpt(M, N, type))
+        return rc;
+    return run_ckpt(true, M, N, type, tg::kActNone, src, q, scales, stream);
+}
+
+int gemm_ckpt_unpack(int64_t M, int64_t N, int type, int epilogue, const void *q, const void *scales, void *out,
+                     hipStream_t stream)
+{
+    if (int rc = check_ckpt(M, N, type))
+        return rc;
+    if (epilogue < GEMM_EPI_NONE || epilogue > GEMM_EPI_BIAS_GELU)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "unknown epilogue %d", epilogue);
+    return run_ckpt(false, M, N, type, act_of(epilogue), out, q, scales, stream);
 }
 
 }  // extern "C"

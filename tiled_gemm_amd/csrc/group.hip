@@ -1,6 +1,7 @@
 // The memory-bound operators around the grouped products: the routing tables
 // (a stable counting sort by expert), the weighted sum of a token's rows and
 // its gradient, and the gradient of the fused epilogue.
+#include "cols.hpp"
 #include "group.hpp"
 
 namespace tg {
@@ -160,42 +161,7 @@ hipError_t launch_group_sort(const SortArgs &a, hipStream_t s)
     return hipGetLastError();
 }
 
-// ---------------------------------------------------------------------------
-// Eight consecutive columns of a bf16 or fp32 row as fp32, and back.
-// ---------------------------------------------------------------------------
 namespace {
-
-template <int T>
-__device__ inline void load8(const void *base, size_t at, float (&v)[8])
-{
-    if constexpr (T == kOutF32) {
-        const f32x4 lo = *(const f32x4 *)((const float *)base + at), hi = *(const f32x4 *)((const float *)base + at + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = lo[i];
-            v[4 + i] = hi[i];
-        }
-    } else {
-        const u32x4 w = *(const u32x4 *)((const uint16_t *)base + at);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bf16_lo(w[i]);
-            v[2 * i + 1] = bf16_hi(w[i]);
-        }
-    }
-}
-
-template <int T>
-__device__ inline void store8(void *base, size_t at, const float (&v)[8])
-{
-    if constexpr (T == kOutF32) {
-        *(f32x4 *)((float *)base + at) = f32x4{v[0], v[1], v[2], v[3]};
-        *(f32x4 *)((float *)base + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
-    } else {
-        *(u32x4 *)((uint16_t *)base + at) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
-    }
-}
 
 constexpr int kCombineThreads = 256;
 // A launch has fewer than 2^32 threads.
@@ -346,8 +312,8 @@ hipError_t launch_group_combine_grad(const CombineArgs &args, hipStream_t s)
 }
 
 // ---------------------------------------------------------------------------
-// d_z = d_c * act'(z) and its column sums per row group.  Bound: HBM (6 bytes
-// per element in bf16).  Rows are cut into chunks that never cross a group; a
+// d_z = d_c * act'(z) and its column sums per row group, z as saved or from its
+// 8-bit checkpoint (CK).  Bound: HBM (6 bytes per element in bf16, 5.03 with CK).  Rows are cut into chunks that never cross a group; a
 // workgroup takes one chunk and 512 columns, lane l of each of its 4 waves
 // columns 8 l .. 8 l + 7, wave w the chunk's rows w, w + 4, ...  The chunk's
 // column sums go to the workspace and a second, small launch adds a group's
@@ -384,7 +350,7 @@ __device__ inline float act_slope(float z)
 
 }  // namespace
 
-template <int T, int ACT>
+template <int T, int ACT, bool CK>
 __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs a)
 {
     __shared__ float red[kActWaves][kActCols];
@@ -411,7 +377,11 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs
             load8<T>(a.d_c, at, d);
             if constexpr (ACT != kActNone) {
                 float z[8];
-                load8<T>(a.z, at, z);
+                if constexpr (CK)
+                    ckpt_load8((const uint8_t *)a.z, at,
+                               e8m0_value(a.scales[(size_t)(r0 + r) * a.blocks + col / kCkptBlock]), z);
+                else
+                    load8<T>(a.z, at, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     d[i] *= act_slope<ACT>(z[i]);
@@ -475,18 +445,18 @@ __global__ __launch_bounds__(kActThreads) void act_grad_bias_kernel(const ActGra
             (red[0][threadIdx.x] + red[1][threadIdx.x]) + (red[2][threadIdx.x] + red[3][threadIdx.x]);
 }
 
-template <int T>
+template <int T, bool CK>
 static void launch_act(const ActGradArgs &a, dim3 grid, hipStream_t s)
 {
     const dim3 threads(kActThreads);
     if (a.act == kActRelu)
-        hipLaunchKernelGGL((act_grad_kernel<T, kActRelu>), grid, threads, 0, s, a);
+        hipLaunchKernelGGL((act_grad_kernel<T, kActRelu, CK>), grid, threads, 0, s, a);
     else if (a.act == kActSilu)
-        hipLaunchKernelGGL((act_grad_kernel<T, kActSilu>), grid, threads, 0, s, a);
+        hipLaunchKernelGGL((act_grad_kernel<T, kActSilu, CK>), grid, threads, 0, s, a);
     else if (a.act == kActGelu)
-        hipLaunchKernelGGL((act_grad_kernel<T, kActGelu>), grid, threads, 0, s, a);
+        hipLaunchKernelGGL((act_grad_kernel<T, kActGelu, CK>), grid, threads, 0, s, a);
     else
-        hipLaunchKernelGGL((act_grad_kernel<T, kActNone>), grid, threads, 0, s, a);
+        hipLaunchKernelGGL((act_grad_kernel<T, kActNone, false>), grid, threads, 0, s, a);
 }
 
 hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s)
@@ -494,9 +464,9 @@ hipError_t launch_act_grad(const ActGradArgs &a, hipStream_t s)
     if (a.max_chunks > 0) {
         const dim3 grid((unsigned)a.max_chunks, (unsigned)((a.N + kActCols - 1) / kActCols));
         if (a.type == kOutF32)
-            launch_act<kOutF32>(a, grid, s);
+            a.scales ? launch_act<kOutF32, true>(a, grid, s) : launch_act<kOutF32, false>(a, grid, s);
         else
-            launch_act<kOutBf16>(a, grid, s);
+            a.scales ? launch_act<kOutBf16, true>(a, grid, s) : launch_act<kOutBf16, false>(a, grid, s);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess)
             return e;

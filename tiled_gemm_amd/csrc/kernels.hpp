@@ -193,7 +193,10 @@ hipError_t launch_group_combine(const CombineArgs &, hipStream_t);
 hipError_t launch_group_combine_grad(const CombineArgs &, hipStream_t);
 
 struct ActGradArgs {
-    const void *d_c, *z;
+    const void *d_c;
+    const void *z;              // M x N of the type, or with scales the checkpoint's e4m3 elements
+    const uint8_t *scales;      // nullptr, or the checkpoint's M x blocks E8M0 bytes
+    int64_t blocks;             // ceil(N / 32)
     void *d_z;
     float *d_bias;              // nullptr or groups x N
     float *partial;             // max_chunks x N (workspace); nullptr without d_bias
@@ -204,6 +207,20 @@ struct ActGradArgs {
     int32_t act, type;
 };
 hipError_t launch_act_grad(const ActGradArgs &, hipStream_t);
+
+// The 8-bit checkpoint (ckpt.hip).
+struct CkptArgs {
+    const void *src;            // pack: M x N of the type
+    void *out;                  // unpack: M x N of the type
+    uint8_t *q;                 // M x N e4m3 elements
+    uint8_t *scales;            // M x blocks E8M0 bytes
+    int64_t M, N, blocks;
+    int32_t act, type;
+    uint32_t units, chunks;     // set by the launchers: waves' work items, and those of one row
+};
+int64_t ckpt_units(int64_t M, int64_t N);      // work items of one launch (the launchers need fewer than 2^31)
+hipError_t launch_ckpt_pack(const CkptArgs &, hipStream_t);
+hipError_t launch_ckpt_unpack(const CkptArgs &, hipStream_t);
 
 constexpr int kSkinnyTileN = 32;
 constexpr int kTiledThreads = 256;
