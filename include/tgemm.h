@@ -448,7 +448,8 @@ int gemm_run_mx_res(const gemm_plan *plan, const void *A, const void *A_bscale, 
 
 typedef enum {
     GEMM_TYPE_F32 = 0,
-    GEMM_TYPE_BF16 = 1
+    GEMM_TYPE_BF16 = 1,
+    GEMM_TYPE_E4M3 = 2          /* weights of gemm_group_mlp_run only */
 } gemm_type;
 
 typedef struct gemm_group_plan gemm_group_plan;   /* opaque, immutable after creation */
@@ -593,6 +594,94 @@ int gemm_group_combine(int64_t tokens, int topk, int64_t N, int type, const void
 int gemm_group_combine_grad(int64_t tokens, int topk, int64_t N, int type, const void *d_out, const void *src,
                             int64_t src_rows, const int32_t *slot_row, const float *weights, void *d_src,
                             float *d_weights, hipStream_t stream);
+
+/*
+ * gemm_group_mlp_* -- a whole mixture-of-experts layer for a few tokens
+ * (decode), two launches without routing tables: slot s = t * topk + j holds
+ * token t's j-th expert e = ids[s],
+ *
+ *   gated:  h[s][n] = cvt( act(g[s][n]) * u[s][n] )       else  h[s][n] = cvt( act(u[s][n]) )
+ *   g[s][n] = (sum_k x[t][k] * up[e][n][k])     * up_scale[e][n]     + up_bias[e][n]
+ *   u[s][n] = (sum_k x[t][k] * up[e][N + n][k]) * up_scale[e][N + n] + up_bias[e][N + n]      (not gated: n for N + n)
+ *   o[s][k] = (sum_n h[s][n] * down[e][k][n])   * down_scale[e][k]   + down_bias[e][k]
+ *   out[t][k] = cvt( sum over j of weights[t][j] * o[s][k]  (+ residual[t][k]) )
+ *
+ * sums, scales, biases and activations in fp32; h is rounded to bf16 (as the
+ * chain of single products keeps it), o is not.  The sum over j runs in the
+ * order of j, the residual last.  A slot whose id is outside 0 .. groups - 1
+ * contributes nothing (nor is its weight read as a factor).  The result does
+ * not depend on scheduling: every run gives the same bits.  For more tokens
+ * use gemm_group_sort, gemm_group_run and gemm_group_combine.
+ *
+ * gemm_group_mlp_plan_create
+ *   groups   1 .. GEMM_GROUP_MAX;  tokens 0 .. GEMM_GROUP_MLP_MAX_TOKENS;
+ *   topk     1 .. GEMM_GROUP_MLP_MAX_TOPK;
+ *   K, N     the model's width and an expert's hidden width, 1 .. 2^20;
+ *            multiples of 32 (bf16 weights) or 64 (e4m3);
+ *            tokens * topk * N < 2^30.
+ *   weight_type  GEMM_TYPE_BF16 or GEMM_TYPE_E4M3 (products exact, as bf16).
+ *   layout   GEMM_LAYOUT_BT or GEMM_LAYOUT_BT_PRESHUFFLED, of both matrices.
+ *   gated    1: up holds 2 N rows per expert (the N gate rows first); 0: N.
+ *   epilogue a gemm_epilogue: which activation (NONE and BIAS: none).
+ * Host only.  NULL on error; freed with gemm_group_mlp_plan_destroy.
+ */
+#define GEMM_GROUP_MLP_MAX_TOKENS 64
+#define GEMM_GROUP_MLP_MAX_TOPK 64
+
+typedef struct gemm_group_mlp_plan gemm_group_mlp_plan;   /* opaque, immutable after creation */
+
+gemm_group_mlp_plan *gemm_group_mlp_plan_create(int groups, int64_t tokens, int topk, int64_t K, int64_t N,
+                                                int weight_type, int layout, int gated, int epilogue);
+void gemm_group_mlp_plan_destroy(gemm_group_mlp_plan *plan);
+
+typedef struct {
+    int64_t tokens, K, N;
+    int32_t groups, topk, weight_type, layout, gated, epilogue;
+} gemm_group_mlp_plan_info;
+int gemm_group_mlp_plan_query(const gemm_group_mlp_plan *plan, gemm_group_mlp_plan_info *info);
+
+/* gemm_group_mlp_workspace_bytes -- bytes gemm_group_mlp_run needs (0: no tokens, or NULL). */
+size_t gemm_group_mlp_workspace_bytes(const gemm_group_mlp_plan *plan);
+
+/*
+ * gemm_group_mlp_preshuffle -- the pre-shuffled images of both matrices (each
+ * as large as its source; gemm_group_preshuffle_b on each, whose errors it
+ * has).  For plans with GEMM_LAYOUT_BT_PRESHUFFLED.
+ */
+int gemm_group_mlp_preshuffle(const gemm_group_mlp_plan *plan, const void *up, void *up_image, const void *down,
+                              void *down_image, hipStream_t stream);
+
+/*
+ * gemm_group_mlp_weights -- the experts' matrices (device pointers).
+ *   up    groups x (gated ? 2 N : N) x K;  down  groups x K x N; each as is or
+ *         its image, as the plan's layout says; 16-byte aligned.
+ *   up_scale, up_bias      groups x (gated ? 2 N : N) floats, or NULL (1, 0);
+ *   down_scale, down_bias  groups x K floats, or NULL (1, 0).
+ */
+typedef struct {
+    const void *up;
+    const void *down;
+    const float *up_scale;
+    const float *down_scale;
+    const float *up_bias;
+    const float *down_bias;
+} gemm_group_mlp_weights;
+
+/*
+ * gemm_group_mlp_run -- the layer on `stream`.
+ *   x         tokens x K bf16, 16-byte aligned;  ids  tokens x topk ints;
+ *   weights   tokens x topk floats (the router's), or NULL (1);
+ *   mats      host pointer, read during the call only;
+ *   residual  tokens x K bf16, 16-byte aligned, or NULL; may be out itself;
+ *   out       tokens x K bf16, 16-byte aligned, overlapping no other operand;
+ *   workspace gemm_group_mlp_workspace_bytes(plan) bytes, 16-byte aligned,
+ *             contents undefined before and after.  Calls that share one must
+ *             not overlap in time.
+ * Asynchronous; allocates nothing; two launches.  GEMM_OK or an error.
+ */
+int gemm_group_mlp_run(const gemm_group_mlp_plan *plan, const void *x, const int32_t *ids, const float *weights,
+                       const gemm_group_mlp_weights *mats, const void *residual, void *out, void *workspace,
+                       size_t workspace_bytes, hipStream_t stream);
 
 /*
  * gemm_act_grad -- the gradient of the fused epilogue, from the saved

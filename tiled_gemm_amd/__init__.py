@@ -58,6 +58,8 @@ EXPORTS = (
     "gemm_group_plan_create", "gemm_group_plan_create_opt", "gemm_group_plan_destroy", "gemm_group_plan_query",
     "gemm_group_preshuffled_b_bytes", "gemm_group_preshuffle_b", "gemm_group_run", "gemm_group_sort_workspace_bytes",
     "gemm_group_sort", "gemm_group_combine", "gemm_group_combine_grad", "gemm_act_grad_workspace_bytes",
+    "gemm_group_mlp_plan_create", "gemm_group_mlp_plan_destroy", "gemm_group_mlp_plan_query",
+    "gemm_group_mlp_workspace_bytes", "gemm_group_mlp_preshuffle", "gemm_group_mlp_run",
     "gemm_act_grad", "gemm_ckpt_pack", "gemm_ckpt_unpack", "gemm_act_grad_ckpt",
 )
 
@@ -65,7 +67,9 @@ GEMM_STATIC_WORKSPACE_BYTES = 64 << 20
 
 GEMM_GROUP_MAX = 1024
 GEMM_GROUP_MAX_ROWS = 1 << 24
-GEMM_TYPE_F32, GEMM_TYPE_BF16 = range(2)
+GEMM_TYPE_F32, GEMM_TYPE_BF16, GEMM_TYPE_E4M3 = range(3)
+GEMM_GROUP_MLP_MAX_TOKENS = 64
+GEMM_GROUP_MLP_MAX_TOPK = 64
 
 
 class GemmError(RuntimeError):
@@ -102,6 +106,18 @@ class gemm_group_plan_info(ctypes.Structure):
 
     def as_dict(self) -> dict:
         return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class gemm_group_mlp_plan_info(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64)] + [
+        (f, ctypes.c_int32) for f in ("groups", "topk", "weight_type", "layout", "gated", "epilogue")]
+
+    def as_dict(self) -> dict:
+        return {f: getattr(self, f) for f, _ in self._fields_}
+
+
+class gemm_group_mlp_weights(ctypes.Structure):
+    _fields_ = [(f, ctypes.c_void_p) for f in ("up", "down", "up_scale", "down_scale", "up_bias", "down_bias")]
 
 
 _lib = None
@@ -148,6 +164,13 @@ def load() -> ctypes.CDLL:
         "gemm_group_combine_grad": (c_int, [i64, c_int, i64, c_int, vp, vp, i64, vp, vp, vp, vp, vp]),
         "gemm_act_grad_workspace_bytes": (ctypes.c_size_t, [i64, i64, c_int]),
         "gemm_act_grad": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp, c_int, vp, vp, ctypes.c_size_t, vp]),
+        "gemm_group_mlp_plan_create": (vp, [c_int, i64, c_int, i64, i64, c_int, c_int, c_int, c_int]),
+        "gemm_group_mlp_plan_destroy": (None, [vp]),
+        "gemm_group_mlp_plan_query": (c_int, [vp, ctypes.POINTER(gemm_group_mlp_plan_info)]),
+        "gemm_group_mlp_workspace_bytes": (ctypes.c_size_t, [vp]),
+        "gemm_group_mlp_preshuffle": (c_int, [vp, vp, vp, vp, vp, vp]),
+        "gemm_group_mlp_run": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_group_mlp_weights), vp, vp, vp,
+                                       ctypes.c_size_t, vp]),
         "gemm_ckpt_pack": (c_int, [i64, i64, c_int, vp, vp, vp, vp]),
         "gemm_ckpt_unpack": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp]),
         "gemm_act_grad_ckpt": (c_int, [i64, i64, c_int, c_int, vp, vp, vp, vp, vp, c_int, vp, vp, ctypes.c_size_t, vp]),
@@ -348,6 +371,43 @@ def gemm_group_combine_grad(tokens: int, topk: int, N: int, type: int, d_out: in
            "gemm_group_combine_grad")
 
 
+def gemm_group_mlp_plan_create(groups: int, tokens: int, topk: int, K: int, N: int, weight_type: int, layout: int,
+                               gated: bool, epilogue: int) -> int:
+    h = load().gemm_group_mlp_plan_create(groups, tokens, topk, K, N, weight_type, layout, int(gated), epilogue)
+    if not h:
+        raise GemmError(-1, "gemm_group_mlp_plan_create", gemm_last_error())
+    return h
+
+
+def gemm_group_mlp_plan_destroy(plan: int) -> None:
+    load().gemm_group_mlp_plan_destroy(plan)
+
+
+def gemm_group_mlp_plan_query(plan: int) -> dict:
+    info = gemm_group_mlp_plan_info()
+    _check(load().gemm_group_mlp_plan_query(plan, ctypes.byref(info)), "gemm_group_mlp_plan_query")
+    return info.as_dict()
+
+
+def gemm_group_mlp_workspace_bytes(plan: int) -> int:
+    return int(load().gemm_group_mlp_workspace_bytes(plan))
+
+
+def gemm_group_mlp_preshuffle(plan: int, up: int, up_image: int, down: int, down_image: int, stream: int = 0) -> None:
+    _check(load().gemm_group_mlp_preshuffle(plan, up, up_image, down, down_image, stream),
+           "gemm_group_mlp_preshuffle")
+
+
+def gemm_group_mlp_run(plan: int, x: int, ids: int, up: int, down: int, out: int, weights: int | None = None,
+                       up_scale: int | None = None, down_scale: int | None = None, up_bias: int | None = None,
+                       down_bias: int | None = None, residual: int | None = None, workspace: int | None = None,
+                       workspace_bytes: int = 0, stream: int = 0) -> None:
+    mats = gemm_group_mlp_weights(up or None, down or None, up_scale or None, down_scale or None, up_bias or None,
+                                  down_bias or None)
+    _check(load().gemm_group_mlp_run(plan, x, ids, weights or None, ctypes.byref(mats), residual or None, out,
+                                     workspace or None, workspace_bytes, stream), "gemm_group_mlp_run")
+
+
 def gemm_act_grad_workspace_bytes(M: int, N: int, groups: int = 1) -> int:
     return int(load().gemm_act_grad_workspace_bytes(M, N, groups))
 
@@ -540,3 +600,41 @@ class GroupPlan:
             preact: int | None = None, stream: int = 0, **epi) -> None:
         """gemm_group_run; epilogue keyword arguments as for the module-level gemm_run_ex."""
         gemm_group_run(self.handle, A, B, C, offsets, row_index, a_rows, preact, stream=stream, **epi)
+
+
+class GroupMlpPlan:
+    """Owns one plan of a mixture-of-experts layer for a few tokens; ``with
+    GroupMlpPlan(...) as p:`` destroys it on exit."""
+
+    def __init__(self, groups: int, tokens: int, topk: int, K: int, N: int, weight_type: int, layout: int,
+                 gated: bool, epilogue: int):
+        self.handle = 0                      # set before create, which may raise
+        self.handle = gemm_group_mlp_plan_create(groups, tokens, topk, K, N, weight_type, layout, gated, epilogue)
+
+    def close(self):
+        h, self.handle = self.handle, 0
+        # At interpreter exit the module's globals may already be cleared.
+        destroy = globals().get("gemm_group_mlp_plan_destroy")
+        if h and destroy is not None:
+            destroy(h)
+
+    __del__ = close
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    def info(self) -> dict:
+        return gemm_group_mlp_plan_query(self.handle)
+
+    def workspace_bytes(self) -> int:
+        return gemm_group_mlp_workspace_bytes(self.handle)
+
+    def preshuffle(self, up: int, up_image: int, down: int, down_image: int, stream: int = 0) -> None:
+        gemm_group_mlp_preshuffle(self.handle, up, up_image, down, down_image, stream)
+
+    def run(self, x: int, ids: int, up: int, down: int, out: int, stream: int = 0, **args) -> None:
+        """gemm_group_mlp_run; keyword arguments as for the module-level function."""
+        gemm_group_mlp_run(self.handle, x, ids, up, down, out, stream=stream, **args)

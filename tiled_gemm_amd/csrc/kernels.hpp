@@ -222,6 +222,33 @@ int64_t ckpt_units(int64_t M, int64_t N);      // work items of one launch (the 
 hipError_t launch_ckpt_pack(const CkptArgs &, hipStream_t);
 hipError_t launch_ckpt_unpack(const CkptArgs &, hipStream_t);
 
+// A mixture-of-experts layer for a few tokens (mlp.hip).
+constexpr int kMlpTokens = 64;
+constexpr int kMlpTopk = 64;
+constexpr int kMlpSlots = kMlpTokens * kMlpTopk;
+constexpr int kMlpTileN = 32;               // weight rows of one work item
+constexpr int kMlpGrid = 512;               // two workgroups per CU
+struct MlpArgs {
+    const void *x;                          // tokens x K bf16
+    const int32_t *ids;                     // slots = tokens x topk
+    const float *weights;                   // nullptr (1) or slots
+    const void *up, *down;                  // groups x (2 N or N) x K, groups x K x N
+    const float *up_scale, *down_scale;     // nullptr or per weight row
+    const float *up_bias, *down_bias;
+    const void *residual;                   // nullptr or tokens x K bf16
+    void *out;                              // tokens x K bf16
+    void *h;                                // workspace: slots x N bf16
+    float *y;                               // workspace: slots x K
+    int32_t *done;                          // workspace: one counter per column tile of out
+    int32_t groups, tokens, topk, slots;
+    int32_t K, N;                           // the model's width, the experts' hidden width
+    int32_t up_tiles, down_tiles;
+    int32_t parts;                          // an upper bound on the active experts
+    int32_t act;
+    bool gated, e4m3, preshuffled;
+};
+hipError_t launch_mlp(const MlpArgs &, hipStream_t);
+
 constexpr int kSkinnyTileN = 32;
 constexpr int kTiledThreads = 256;
 
