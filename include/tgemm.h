@@ -335,6 +335,51 @@ int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, voi
                         const gemm_epilogue_args *epi, hipStream_t stream);
 
 /*
+ * gemm_run_lora -- gemm_run_res with the low-rank adapters of many requests
+ * beside the shared B.  Row m of A belongs to adapter a = adapter[m]:
+ *
+ *   v[m][r] = scale[a] * sum_k A[m][k] * down[a][r][k]                       (fp32)
+ *   z[m][n] = sum_k A[m][k] * b(n,k)  +  sum_r v[m][r] * up[a][n][r]  (+ bias[n])
+ *   C[m][n] = cvt( act(z[m][n])  (+ residual[m][n]) )          preact[m][n] = cvt( z[m][n] )
+ *
+ * Both sums over r and k are fp32; v is not rounded to bf16 (it enters the
+ * second product as a sum of two bf16 numbers).  A row whose adapter is outside
+ * 0 .. adapters - 1 has none.  Rows of different adapters may be mixed in any
+ * order; an adapter's infinities and NaN reach its own rows only.
+ *   adapter  device pointer, M ints;
+ *   down     adapters x rank x K bf16, up  adapters x N x rank bf16, 16-byte
+ *            aligned (adapters of a lower rank are filled up with zeros);
+ *   scale    device pointer, adapters floats, or NULL (1);
+ *   adapters 1 .. GEMM_LORA_MAX_ADAPTERS;
+ *   rank     a multiple of 8, 8 .. GEMM_LORA_MAX_RANK.
+ * Plans: bf16 (either output type) with GEMM_LAYOUT_BT or
+ * GEMM_LAYOUT_BT_PRESHUFFLED, M <= GEMM_GROUP_MAX_ROWS.  epi has no scales.
+ *   residual, preact  as for gemm_run_res;
+ *   workspace  gemm_lora_workspace_bytes(plan, rank) bytes, 16-byte aligned,
+ *            contents undefined before and after (v, and the partial tiles
+ *            where the plan splits K).  Calls that share one must not overlap
+ *            in time.
+ * Asynchronous; allocates nothing; two launches (three with split K).  GEMM_OK
+ * or an error.
+ */
+#define GEMM_LORA_MAX_ADAPTERS 65536
+#define GEMM_LORA_MAX_RANK 256
+
+typedef struct {
+    const int32_t *adapter;
+    const void *down;
+    const void *up;
+    const float *scale;
+    int32_t adapters;
+    int32_t rank;
+} gemm_lora_args;
+
+size_t gemm_lora_workspace_bytes(const gemm_plan *plan, int rank);
+int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
+                  const gemm_lora_args *lora, const void *residual, void *preact, void *workspace,
+                  size_t workspace_bytes, hipStream_t stream);
+
+/*
  * MX block-scaled operands (GEMM_MXFP8_OUT_BF16, GEMM_MXFP4_OUT_BF16).  The
  * pages' gfx950 scaled MFMA (FlyDSL "Kernel authoring guide", section 4.3
  * "ROCm intrinsics", MFMA instructions: mfma_scale_f32_16x16x128_f8f6f4)

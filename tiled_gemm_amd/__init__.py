@@ -55,6 +55,7 @@ EXPORTS = (
     "gemm_last_error", "gemm_plan_query", "gemm_plan_layout", "gemm_layout_crd2idx",
     "gemm_layout_idx2crd", "gemm_lds_swizzle", "gemm_tile_of_workgroup", "gemm_workspace_bytes",
     "gemm_run_ws", "gemm_run_ws_noalloc", "gemm_run_res", "gemm_run_mx_res",
+    "gemm_lora_workspace_bytes", "gemm_run_lora",
     "gemm_group_plan_create", "gemm_group_plan_create_opt", "gemm_group_plan_destroy", "gemm_group_plan_query",
     "gemm_group_preshuffled_b_bytes", "gemm_group_preshuffle_b", "gemm_group_run", "gemm_group_sort_workspace_bytes",
     "gemm_group_sort", "gemm_group_combine", "gemm_group_combine_grad", "gemm_act_grad_workspace_bytes",
@@ -64,6 +65,9 @@ EXPORTS = (
 )
 
 GEMM_STATIC_WORKSPACE_BYTES = 64 << 20
+
+GEMM_LORA_MAX_ADAPTERS = 65536
+GEMM_LORA_MAX_RANK = 256
 
 GEMM_GROUP_MAX = 1024
 GEMM_GROUP_MAX_ROWS = 1 << 24
@@ -82,6 +86,11 @@ class gemm_epilogue_args(ctypes.Structure):
     _fields_ = [("scale_a", ctypes.c_void_p), ("scale_b", ctypes.c_void_p), ("bias", ctypes.c_void_p),
                 ("scale_a_per_row", ctypes.c_int32), ("scale_b_per_col", ctypes.c_int32),
                 ("epilogue", ctypes.c_int32)]
+
+
+class gemm_lora_args(ctypes.Structure):
+    _fields_ = [("adapter", ctypes.c_void_p), ("down", ctypes.c_void_p), ("up", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("adapters", ctypes.c_int32), ("rank", ctypes.c_int32)]
 
 
 class gemm_plan_options(ctypes.Structure):
@@ -151,6 +160,9 @@ def load() -> ctypes.CDLL:
         "gemm_run_ws_noalloc": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp]),
         "gemm_run_res": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp, vp, vp, ctypes.c_size_t, vp]),
         "gemm_run_mx_res": (c_int, [vp, vp, vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), vp, vp, vp]),
+        "gemm_lora_workspace_bytes": (ctypes.c_size_t, [vp, c_int]),
+        "gemm_run_lora": (c_int, [vp, vp, vp, vp, ctypes.POINTER(gemm_epilogue_args), ctypes.POINTER(gemm_lora_args),
+                                  vp, vp, vp, ctypes.c_size_t, vp]),
         "gemm_group_plan_create": (vp, [c_int, i64, i64, i64, c_int, c_int]),
         "gemm_group_plan_create_opt": (vp, [c_int, i64, i64, i64, c_int, c_int, c_int]),
         "gemm_group_plan_destroy": (None, [vp]),
@@ -277,6 +289,22 @@ def gemm_run_res(plan: int, A: int, B: int, C: int, residual: int | None = None,
                              int(scale_b_per_col), epilogue)
     _check(load().gemm_run_res(plan, A, B, C, ctypes.byref(epi), residual or None, preact or None, workspace or None,
                                workspace_bytes, stream), "gemm_run_res")
+
+
+def gemm_lora_workspace_bytes(plan: int, rank: int) -> int:
+    return int(load().gemm_lora_workspace_bytes(plan, rank))
+
+
+def gemm_run_lora(plan: int, A: int, B: int, C: int, adapter: int, adapters: int, rank: int, down: int, up: int,
+                  scale: int | None = None, residual: int | None = None, preact: int | None = None,
+                  workspace: int | None = None, workspace_bytes: int = 0, scale_a: int | None = None,
+                  scale_a_per_row: bool = False, scale_b: int | None = None, scale_b_per_col: bool = False,
+                  bias: int | None = None, epilogue: int = GEMM_EPI_NONE, stream: int = 0) -> None:
+    epi = gemm_epilogue_args(scale_a or None, scale_b or None, bias or None, int(scale_a_per_row),
+                             int(scale_b_per_col), epilogue)
+    lora = gemm_lora_args(adapter or None, down or None, up or None, scale or None, adapters, rank)
+    _check(load().gemm_run_lora(plan, A, B, C, ctypes.byref(epi), ctypes.byref(lora), residual or None, preact or None,
+                                workspace or None, workspace_bytes, stream), "gemm_run_lora")
 
 
 def gemm_bscale_image_bytes(plan: int, operand: int) -> int:
@@ -554,6 +582,14 @@ class Plan:
     def run_mx_res(self, A: int, A_bscale: int, B: int, B_bscale: int, C: int, residual: int | None = None,
                    preact: int | None = None, stream: int = 0, **epi) -> None:
         gemm_run_mx_res(self.handle, A, A_bscale, B, B_bscale, C, residual, preact, stream=stream, **epi)
+
+    def lora_workspace_bytes(self, rank: int) -> int:
+        return gemm_lora_workspace_bytes(self.handle, rank)
+
+    def run_lora(self, A: int, B: int, C: int, adapter: int, adapters: int, rank: int, down: int, up: int,
+                 stream: int = 0, **args) -> None:
+        """gemm_run_lora; keyword arguments as for the module-level function."""
+        gemm_run_lora(self.handle, A, B, C, adapter, adapters, rank, down, up, stream=stream, **args)
 
     def run_ws_noalloc(self, A: int, B: int, C: int, stream: int = 0, **epi) -> None:
         """gemm_run_ws_noalloc; keyword arguments as for the module-level gemm_run_ex."""

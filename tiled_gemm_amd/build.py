@@ -19,7 +19,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libtgemm.so")
 SOURCES = ["capi.cpp", "gemm_tiled.hip", "gemm_pipe.hip", "gemm_dma.hip", "gemm_skinny.hip", "preshuffle.hip",
            "splitk.hip", "gemm_mxw.hip", "capi_group.cpp", "group.hip", "gemm_group.hip", "ckpt.hip",
-           "capi_mlp.cpp", "mlp.hip"]
+           "capi_mlp.cpp", "mlp.hip", "lora.hip"]
 ARCH = "gfx950"
 
 COMMON_FLAGS = [

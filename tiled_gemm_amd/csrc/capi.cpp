@@ -743,13 +743,16 @@ int gemm_preshuffle_b(const gemm_plan *plan, const void *B, void *B_shuf, hipStr
 
 namespace {
 
+// lora: nullptr, or the adapters' operands (their first half already on the
+// stream; the plan's kernel has the second).
 int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const tg::EpiArgs &epi,
-             hipStream_t stream, const void *sa_img = nullptr, const void *sb_img = nullptr)
+             hipStream_t stream, const void *sa_img = nullptr, const void *sb_img = nullptr,
+             const tg::LoraArgs *lora = nullptr)
 {
     if (!plan)
         return fail(GEMM_ERR_INVALID_ARG, "NULL plan");
     const gemm_plan_info &I = plan->info;
-    const bool ex = epi.res || epi.pre;
+    const bool ex = epi.res || epi.pre || lora;
     if (I.M == 0 || I.N == 0) {
         ok();
         return GEMM_OK;
@@ -785,7 +788,9 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         a.sa_img = (const uint8_t *)sa_img;
         a.sb_img = (const uint8_t *)sb_img;
         a.s_groups = (int32_t)scale_groups(I.K);
-        e = (ex ? plan->skinny->launch_ex : plan->skinny->launch)(a, I.grid, stream);
+        if (lora)
+            a.lora = *lora;
+        e = (lora ? plan->skinny->launch_lora : ex ? plan->skinny->launch_ex : plan->skinny->launch)(a, I.grid, stream);
     } else {
         tg::TiledArgs a{};
         a.A = A;
@@ -808,7 +813,9 @@ int run_impl(const gemm_plan *plan, const void *A, const void *B, void *C, const
         a.sa_img = (const uint8_t *)sa_img;
         a.sb_img = (const uint8_t *)sb_img;
         a.s_groups = (int32_t)scale_groups(I.K);
-        e = ex ? plan->ex_v->launch_ex(a, stream) : plan->tiled->launch(a, stream);
+        if (lora)
+            a.lora = *lora;
+        e = (lora ? plan->ex_v->launch_lora : ex ? plan->ex_v->launch_ex : plan->tiled->launch)(a, stream);
     }
     if (e != hipSuccess)
         return fail(GEMM_ERR_HIP, "kernel launch: %s", hipGetErrorString(e));
@@ -828,7 +835,7 @@ size_t workspace_bytes(const gemm_plan *plan)
 // Split-K run: the slices' fp32 partials into W, then the ordered sum and
 // the epilogue into C.  The caller has validated A, B, C and W.
 int run_split(const gemm_plan *plan, const void *A, const void *B, void *C, void *W, const tg::EpiArgs &epi,
-              hipStream_t stream)
+              hipStream_t stream, const tg::LoraArgs *lora = nullptr)
 {
     const gemm_plan_info &I = plan->info;
     tg::TiledArgs a{};
@@ -852,7 +859,9 @@ int run_split(const gemm_plan *plan, const void *A, const void *B, void *C, void
     a.group_m = plan->split_group_m;
     a.splits = plan->splits;
     a.split_steps = plan->split_steps;
-    hipError_t e = plan->split_v->launch(a, stream);
+    if (lora)
+        a.lora = *lora;
+    hipError_t e = (lora ? plan->split_v->launch_lora_part : plan->split_v->launch)(a, stream);
     if (e != hipSuccess)
         return fail(GEMM_ERR_HIP, "split-K launch: %s", hipGetErrorString(e));
     tg::SplitReduceArgs r{};
@@ -950,6 +959,22 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
     return GEMM_OK;
 }
 
+// K is shared out over this many workgroups in the adapters' first half, where
+// each has one adapter: 64 KiB of 16 ranks each.
+int lora_parts(int64_t M, int64_t K)
+{
+    if (M > tg::kLoraFewRows)
+        return 1;
+    const int64_t p = (K * 2 * 16 + (64 << 10) - 1) / (64 << 10);
+    return (int)(p < 1 ? 1 : p > 8 ? 8 : p);
+}
+
+size_t lora_v_bytes(const gemm_plan *plan, int rank)
+{
+    const size_t n = (size_t)lora_parts(plan->info.M, plan->info.K) * (size_t)plan->info.M * (size_t)((rank + 31) / 32 * 32) * 4;
+    return (n + 255) / 256 * 256;
+}
+
 int check_mx(const gemm_plan *plan, const void *A_bscale, const void *B_bscale)
 {
     if (!plan)
@@ -1036,6 +1061,97 @@ int gemm_run_res(const gemm_plan *plan, const void *A, const void *B, void *C, c
         overlap(workspace, need, preact, preact ? cbytes : 0))
         return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps the residual or preact");
     return run_ws_impl(plan, A, B, C, e, workspace, stream);
+}
+
+size_t gemm_lora_workspace_bytes(const gemm_plan *plan, int rank)
+{
+    if (!plan || plan->info.M == 0 || plan->info.N == 0 || rank < 8 || rank > GEMM_LORA_MAX_RANK || rank % 8 != 0)
+        return 0;
+    return lora_v_bytes(plan, rank) + workspace_bytes(plan);
+}
+
+int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
+                  const gemm_lora_args *lora, const void *residual, void *preact, void *workspace,
+                  size_t workspace_bytes_given, hipStream_t stream)
+{
+    if (int rc = reject_mx(plan))
+        return rc;
+    tg::EpiArgs e;
+    if (int rc = epi_from(epi, &e))
+        return rc;
+    if (int rc = ext_from(plan, A, B, C, residual, preact, &e))
+        return rc;
+    const gemm_plan_info &I = plan->info;
+    if (!lora)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL lora");
+    if ((I.dtype != GEMM_BF16_OUT_BF16 && I.dtype != GEMM_BF16_OUT_F32) ||
+        (I.layout != GEMM_LAYOUT_BT && I.layout != GEMM_LAYOUT_BT_PRESHUFFLED))
+        return fail(GEMM_ERR_UNSUPPORTED, "adapters go with bf16 plans and B stored N x K (or pre-shuffled)");
+    if (e.sa || e.sb)
+        return fail(GEMM_ERR_INVALID_ARG, "gemm_run_lora takes no scale_a or scale_b");
+    if (lora->adapters < 1 || lora->adapters > GEMM_LORA_MAX_ADAPTERS)
+        return fail(GEMM_ERR_INVALID_ARG, "adapters=%d outside 1..%d", (int)lora->adapters, GEMM_LORA_MAX_ADAPTERS);
+    if (lora->rank < 8 || lora->rank > GEMM_LORA_MAX_RANK || lora->rank % 8 != 0)
+        return fail(GEMM_ERR_INVALID_ARG, "rank=%d must be a multiple of 8 in 8..%d", (int)lora->rank,
+                    GEMM_LORA_MAX_RANK);
+    // (N x rank stays below 2^30, for the 32-bit offsets into an adapter's
+    // matrix, by the plan's own bound on N)
+    static_assert(GEMM_LORA_MAX_RANK <= 256, "N < 2^22 from N * out_bytes * 256 < 2^31");
+    if (I.M > GEMM_GROUP_MAX_ROWS)
+        return fail(GEMM_ERR_UNSUPPORTED, "M above 2^24");
+    if (I.M == 0 || I.N == 0)
+        return ok(), GEMM_OK;
+    const bool split = plan->splits > 1;
+    if (split ? !plan->split_v->launch_lora_part
+              : I.kernel == 1 ? !plan->skinny->launch_lora : !plan->ex_v || !plan->ex_v->launch_lora)
+        return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no adapters (GEMM_KERNEL_AUTO, "
+                                          "GEMM_KERNEL_TILE256 and GEMM_KERNEL_GENERIC_128 have)");
+    if (!lora->adapter || (I.K && !lora->down) || !lora->up)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL adapter, down or up");
+    if (!aligned(lora->adapter, 4) || !aligned(lora->scale, 4) || misaligned(lora->up) ||
+        (lora->down && misaligned(lora->down)))
+        return fail(GEMM_ERR_INVALID_ARG, "adapter and scale must be 4-byte aligned, down and up 16");
+    const size_t need = gemm_lora_workspace_bytes(plan, lora->rank);
+    if (!workspace || workspace_bytes_given < need || misaligned(workspace))
+        return fail(GEMM_ERR_INVALID_ARG, "adapters need a 16-byte aligned workspace of %zu bytes", need);
+    const size_t cbytes = (size_t)I.M * I.N * I.out_bytes, n = (size_t)lora->adapters * lora->rank * 2;
+    const struct {
+        const void *p;
+        size_t n;
+    } in[] = {{A, (size_t)I.M * plan->kbytes}, {B, (size_t)I.N * plan->kbytes_b}, {lora->adapter, (size_t)I.M * 4},
+              {lora->down, n * (size_t)I.K},   {lora->up, n * (size_t)I.N},       {lora->scale, (size_t)lora->adapters * 4},
+              {residual, residual == C ? 0 : cbytes}};
+    using tg::capi_overlap;
+    for (const auto &v : in)
+        if (capi_overlap(workspace, need, v.p, v.n) || capi_overlap(C, cbytes, v.p, v.n) ||
+            capi_overlap(preact, cbytes, v.p, v.n))
+            return fail(GEMM_ERR_INVALID_ARG, "the workspace, C or preact overlaps an input");
+    if (capi_overlap(workspace, need, C, cbytes) || capi_overlap(workspace, need, preact, cbytes))
+        return fail(GEMM_ERR_INVALID_ARG, "the workspace overlaps C or preact");
+    if ((I.K && (!A || !B)) || !C)
+        return fail(GEMM_ERR_INVALID_ARG, "NULL A, B or C");
+    if ((A && misaligned(A)) || (B && misaligned(B)) || misaligned(C))
+        return fail(GEMM_ERR_INVALID_ARG, "A, B and C must be 16-byte aligned");
+    if (int rc = check_device())
+        return rc;
+    tg::LoraArgs l{};
+    l.adapter = lora->adapter;
+    l.v = l.v_out = (float *)workspace;
+    l.x = A;
+    l.down = lora->down;
+    l.up = lora->up;
+    l.scale = lora->scale;
+    l.adapters = lora->adapters;
+    l.rank = lora->rank;
+    l.rank_pad = (lora->rank + 31) / 32 * 32;
+    l.M = (int32_t)I.M;
+    l.K = (int32_t)I.K;
+    l.parts = lora_parts(I.M, I.K);
+    const hipError_t r = tg::launch_lora_down(l, stream);
+    if (r != hipSuccess)
+        return fail(GEMM_ERR_HIP, "adapters' launch: %s", hipGetErrorString(r));
+    return split ? run_split(plan, A, B, C, (uint8_t *)workspace + lora_v_bytes(plan, lora->rank), e, stream, &l)
+                 : run_impl(plan, A, B, C, e, stream, nullptr, nullptr, &l);
 }
 
 int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, void *C,

@@ -31,8 +31,7 @@
 //           stage about to be overwritten has returned).
 //   Epilogue (acc * s_a) * s_b (+ bias, activation) in fp32, RNE to bf16,
 //           buffer stores (rows past M and columns past N dropped).
-#include "device.hpp"
-#include "kernels.hpp"
+#include "lora.hpp"
 
 namespace tg {
 
@@ -50,7 +49,7 @@ using dic = std::integral_constant<int, N>;
 
 }  // namespace
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX, bool LORA>
 __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const TiledArgs p)
 {
     static_assert(ELEM == kBf16 || ELEM == kFp8 || (ELEM == kI8 && OUT == kOutBf16),
@@ -421,6 +420,12 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     }
     __builtin_amdgcn_s_waitcnt(0);
 
+    // (of a split K the first slice's partial tile takes the adapters' share)
+    if constexpr (LORA) {
+        if (sk.kt0 == 0)
+            lora_tail<FM, FN>(p.lora, acc, m0, rows_a, wm * WTM, n0 + wn * WTN, p.N);
+    }
+
     // ---- epilogue: row blocks outside, column blocks inside, so a wave
     // writes its adjacent pieces of one C row back to back.
     const EpiView ev = epi_view(p.epi, p.M, p.N);
@@ -466,10 +471,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     }
 }
 
-template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX = false>
+template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int PD, bool BKN, bool AKM, bool EX = false,
+          bool LORA = false>
 static hipError_t launch_dma(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_dma_kernel<ELEM, OUT, BPRE, WGM, WGN, PD, BKN, AKM, EX>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_dma_kernel<ELEM, OUT, BPRE, WGM, WGN, PD, BKN, AKM, EX, LORA>), dim3(a.grid),
                        dim3(64 * WGM * WGN), 0, s, a);
     return hipGetLastError();
 }
@@ -493,9 +499,17 @@ static hipError_t launch_dma(const TiledArgs &a, hipStream_t s)
                  &launch_dma<ELEM, kOutBf16, false, 1, 8, 2, BKN, true>, BKN, true,                     \
                  &launch_dma<ELEM, kOutBf16, false, 1, 8, 2, BKN, true, true>}
 
+// bf16 with B N x K, and low-rank adapters: the extended epilogue, and the
+// split-K partial tiles (fp32 output only).
+#define TG_DMA_LORA(OUT, PD, PART)                                                                  \
+    TiledVariant{DM_BM, DM_BN, 2, 4, kBf16, OUT, false, DM_LDS, 2,                                      \
+                 &launch_dma<kBf16, OUT, false, 2, 4, PD, false, false>, false, false,                  \
+                 &launch_dma<kBf16, OUT, false, 2, 4, PD, false, false, true>,                          \
+                 &launch_dma<kBf16, OUT, false, 2, 4, PD, false, false, true, true>, PART}
+
 static const TiledVariant kDma[] = {
-    TG_DMA(kBf16, kOutBf16, false, 2, 4, 6),   // B N x K
-    TG_DMA(kBf16, kOutF32, false, 2, 4, 4),
+    TG_DMA_LORA(kOutBf16, 6, nullptr),         // B N x K
+    TG_DMA_LORA(kOutF32, 4, (&launch_dma<kBf16, kOutF32, false, 2, 4, 4, false, false, false, true>)),
     TG_DMA(kFp8, kOutBf16, false, 2, 4, 2),    // fp8, B N x K
     // fp8 with fp32 output: split-K partial tiles only, no extended epilogue
     TiledVariant{DM_BM, DM_BN, 2, 4, kFp8, kOutF32, false, DM_LDS, 2,

@@ -33,8 +33,7 @@
 //       vmcnt immediates are exact.
 //   Epilogue as in the generic tiled kernel: (acc * s_a) * s_b, RNE to bf16,
 //   buffer stores (rows past M and columns past N dropped).
-#include "device.hpp"
-#include "kernels.hpp"
+#include "lora.hpp"
 
 #include <type_traits>
 
@@ -71,7 +70,7 @@ using ic = std::integral_constant<int, N>;
 // ADMA: A goes global -> LDS by the load's own LDS write (true) or through
 // VGPRs: loaded at barrier(k), written with ds_write_b128 at barrier(k+1).
 template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD,
-          bool EX>
+          bool EX, bool LORA>
 __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const TiledArgs p)
 {
     using Cfg = BpCfg<WGM, WGN, NS>;
@@ -476,6 +475,11 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
     if constexpr (ACCA)
         mfma_drain_acc(acc);
+    // (of a split K the first slice's partial tile takes the adapters' share)
+    if constexpr (LORA) {
+        if (sk.kt0 == 0)
+            lora_tail<BP_FM, BP_FN>(p.lora, acc, m0, rows_a, wm * BP_WTM, n0 + wn * BP_WTN, p.N);
+    }
 
     // ---- epilogue: scale, bias, activation, convert, store.  Row blocks
     // outside, column blocks inside: a wave writes its adjacent pieces of
@@ -524,10 +528,10 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
 }
 
 template <int ELEM, int OUT, bool BPRE, int WGM, int WGN, int NS, int PD, bool ADMA, bool ACCA, bool SPREAD,
-          bool EX = false>
+          bool EX = false, bool LORA = false>
 static hipError_t launch_pipe(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_pipe_kernel<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, ACCA, SPREAD, EX>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_pipe_kernel<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, ACCA, SPREAD, EX, LORA>), dim3(a.grid),
                        dim3(64 * WGM * WGN), 0, s, a);
     return hipGetLastError();
 }
@@ -540,13 +544,20 @@ static hipError_t launch_pipe(const TiledArgs &a, hipStream_t s)
     TiledVariant{BP_BM, BP_BN, WGM, WGN, ELEM, OUT, BPRE, BpCfg<WGM, WGN, NS>::LDS, NS,          \
                  &launch_pipe<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, (WGM * WGN == 4), SPREAD>, false, false, \
                  &launch_pipe<ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, (WGM * WGN == 4), SPREAD, true>}
+// bf16 pre-shuffled, and low-rank adapters: the extended epilogue, and the
+// split-K partial tiles (fp32 output only)
+#define TG_PIPE_LORA(OUT, PART)                                                                 \
+    TiledVariant{BP_BM, BP_BN, 1, 8, kBf16, OUT, true, BpCfg<1, 8, 4>::LDS, 4,                   \
+                 &launch_pipe<kBf16, OUT, true, 1, 8, 4, 6, true, false, true>, false, false,    \
+                 &launch_pipe<kBf16, OUT, true, 1, 8, 4, 6, true, false, true, true>,            \
+                 &launch_pipe<kBf16, OUT, true, 1, 8, 4, 6, true, false, true, true, true>, PART}
 #define TG_PIPE(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA) TG_PIPE_S(ELEM, OUT, BPRE, WGM, WGN, NS, PD, ADMA, false)
 
 // The first 8-wave and the first 4-wave variant of each (elem, out, layout)
 // are the ones a plan can get; sweep builds add alternatives.
 static const TiledVariant kPipe[] = {
-    TG_PIPE_X(kBf16, kOutBf16, true, 1, 8, 4, 6, true, true),
-    TG_PIPE_X(kBf16, kOutF32, true, 1, 8, 4, 6, true, true),
+    TG_PIPE_LORA(kOutBf16, nullptr),
+    TG_PIPE_LORA(kOutF32, (&launch_pipe<kBf16, kOutF32, true, 1, 8, 4, 6, true, false, true, false, true>)),
     TG_PIPE_S(kBf16, kOutBf16, false, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kBf16, kOutF32, false, 1, 8, 4, 6, true, true),
     TG_PIPE_S(kFp8, kOutBf16, false, 1, 8, 4, 3, true, true),

@@ -26,12 +26,19 @@
 //
 // The partial tiles of the waves are summed through LDS in a fixed wave order
 // (deterministic), then scaled, converted and stored.
-#include "device.hpp"
-#include "kernels.hpp"
+#include "lora.hpp"
 
 namespace tg {
 
 constexpr int kRedPitch = kSkinnyTileN + 1;   // padded reduction row (bank spread)
+
+// Behind low-rank adapters a workgroup has some waves more, which take the
+// adapters' products (lora.hpp) while the others stream B: each of those is a
+// chain of cache latencies, and after the main loop they would add theirs to
+// its time.  Their sums join in the reduction like a slice of K.
+constexpr int kLoraWaves = 4;
+template <int WAVES, bool LORA>
+constexpr int skinny_waves() { return WAVES + (LORA ? kLoraWaves : 0); }
 
 // Sums the waves' partial 16 x 16 tiles through LDS in a fixed wave order
 // (deterministic), then applies the epilogue and stores C.  The caller has
@@ -104,24 +111,24 @@ __device__ inline void skinny_finish(const SkinnyArgs &p, const f32x4 (&acc)[MB]
     }
 }
 
-template <int MB, int WAVES, int DEPTH>
+template <int MB, int WAVES, int DEPTH, bool LORA = false>
 struct SkinnyCfg {
     static constexpr int ROWS_A = MB * 16;
     static constexpr int ROWS = ROWS_A + kSkinnyTileN;      // stage rows: A rows, then B rows
     static constexpr int STAGE = ROWS * kTileKBytes;        // bytes per stage
     static constexpr int RING = DEPTH * STAGE;              // bytes per wave
     static constexpr int LOADS = ROWS / 8;                  // 1 KiB wave loads per stage
-    static constexpr int RED = WAVES * ROWS_A * kRedPitch * 4;
+    static constexpr int RED = skinny_waves<WAVES, LORA>() * ROWS_A * kRedPitch * 4;
     static constexpr int LDS = WAVES * RING > RED ? WAVES * RING : RED;
     static_assert(ROWS_A % 8 == 0, "a wave load must not mix A and B rows");
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX>
-__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const SkinnyArgs p)
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX, bool LORA>
+__global__ __launch_bounds__((64 * skinny_waves<WAVES, LORA>()), 1) void gemm_skinny_kernel(const SkinnyArgs p)
 {
-    using Cfg = SkinnyCfg<MB, WAVES, DEPTH>;
+    using Cfg = SkinnyCfg<MB, WAVES, DEPTH, LORA>;
     constexpr int NB = kSkinnyTileN / 16;
     constexpr int L = Cfg::LOADS;
     __shared__ __attribute__((aligned(1024))) uint8_t lds[Cfg::LDS];
@@ -219,31 +226,51 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_kernel(const Skinny
     constexpr int kVm = (DEPTH - 1) * L;
     constexpr int kWaitOldest = (kWaitVmcnt0 & ~0xC00F) | (kVm & 0xF) | ((kVm >> 4) << 14);
     constexpr int kWaitLds = 0xC07F;                 // lgkmcnt(0) only
+    auto stream = [&]() {
 #pragma unroll
-    for (int s = 0; s < DEPTH; ++s)
-        issue(s, s);
-    int s = 0;
-    for (int t = 0; t < nt; ++t) {
-        __builtin_amdgcn_s_waitcnt(kWaitOldest);
-        compute(s);
-        __builtin_amdgcn_s_waitcnt(kWaitLds);         // the stage's reads are done before its refill
-        issue(t + DEPTH, s);
-        s = s + 1 == DEPTH ? 0 : s + 1;
+        for (int s = 0; s < DEPTH; ++s)
+            issue(s, s);
+        int s = 0;
+        for (int t = 0; t < nt; ++t) {
+            __builtin_amdgcn_s_waitcnt(kWaitOldest);
+            compute(s);
+            __builtin_amdgcn_s_waitcnt(kWaitLds);         // the stage's reads are done before its refill
+            issue(t + DEPTH, s);
+            s = s + 1 == DEPTH ? 0 : s + 1;
+        }
+    };
+    if constexpr (LORA) {
+        if (w < WAVES)
+            stream();
+        else
+            lora_skinny<MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
+    } else {
+        stream();
     }
     // Out-of-range loads still write (zeros) into LDS: drain them before the
     // ring is reused for the reduction.
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);
     __syncthreads();
 
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : 0, EX>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, skinny_waves<WAVES, LORA>(), ELEM == kI8 ? 1 : 0, EX>(p, acc, lds, n0);
 }
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX = false>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE, bool EX = false, bool LORA = false>
 static hipError_t launch_skinny(const SkinnyArgs &a, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_skinny_kernel<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, EX>), dim3(grid), dim3(64 * WAVES), 0,
-                       s, a);
+    hipLaunchKernelGGL((gemm_skinny_kernel<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, EX, LORA>), dim3(grid),
+                       dim3(64 * skinny_waves<WAVES, LORA>()), 0, s, a);
     return hipGetLastError();
+}
+
+using SkinnyLaunch = hipError_t (*)(const SkinnyArgs &, int grid, hipStream_t);
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool ROTATE>
+constexpr SkinnyLaunch skinny_lora()
+{
+    if constexpr (ELEM == kBf16)
+        return &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, true, true>;
+    else
+        return nullptr;
 }
 
 // ---------------------------------------------------------------------------
@@ -256,7 +283,7 @@ static hipError_t launch_skinny(const SkinnyArgs &a, int grid, hipStream_t s)
 // in the MFMA order like the tiled kernels' A.  The step, the K split over
 // the waves, the rotation and the reduction are those of the kernel above.
 // ---------------------------------------------------------------------------
-template <int MB, int WAVES, int DEPTH, bool BLDS, int BH = 2>
+template <int MB, int WAVES, int DEPTH, bool BLDS, int BH = 2, bool LORA = false>
 struct SkinnyPreCfg {
     static constexpr int ROWS_A = MB * 16;
     static constexpr int ASTAGE = ROWS_A * kTileKBytes;     // A bytes per stage
@@ -265,14 +292,14 @@ struct SkinnyPreCfg {
     static constexpr int RING = DEPTH * STAGE;              // bytes per wave
     static constexpr int AL = ROWS_A / 8;                   // 1 KiB A loads per stage
     static constexpr int LOADS = AL + BL;
-    static constexpr int RED = WAVES * ROWS_A * kRedPitch * 4;
+    static constexpr int RED = skinny_waves<WAVES, LORA>() * ROWS_A * kRedPitch * 4;
     static constexpr int LDS = WAVES * RING > RED ? WAVES * RING : RED;
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
     static_assert((DEPTH - 1) * LOADS < 64, "vmcnt holds 6 bits");
 };
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX>
-__global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const SkinnyArgs p)
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX, bool LORA>
+__global__ __launch_bounds__((64 * skinny_waves<WAVES, LORA>()), 1) void gemm_skinny_pre_kernel(const SkinnyArgs p)
 {
     // Packed int4 B (W4A8): one 1 KiB block per 16 columns and step, i.e. the
     // 64 B-bytes of 128 K values per row; lane group q holds values 32 q ..
@@ -295,7 +322,7 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     constexpr int BH = W4 ? 1 : 2;
     static_assert(!INT || OUT == kOutBf16, "integer GEMMs write bf16");
     static_assert(!MX || (DEPTH % SPG == 0 && ORD == 1 && !BLDS), "MX: whole scale groups per ring, runs");
-    using Cfg = SkinnyPreCfg<MB, WAVES, DEPTH, BLDS, BH>;
+    using Cfg = SkinnyPreCfg<MB, WAVES, DEPTH, BLDS, BH, LORA>;
     constexpr int NB = kSkinnyTileN / 16;
     constexpr int AL = Cfg::AL;
     constexpr int LOADS = Cfg::LOADS + (MX ? 2 : 0);
@@ -457,39 +484,59 @@ __global__ __launch_bounds__(64 * WAVES, 1) void gemm_skinny_pre_kernel(const Sk
     constexpr int kWaitOldest = (kWaitVmcnt0 & ~0xC00F) | (kVm & 0xF) | ((kVm >> 4) << 14);
     constexpr int kWaitLds = 0xC07F;
     const int ntr = (nt + DEPTH - 1) / DEPTH * DEPTH;
-    static_for<DEPTH>([&](auto s_c) { issue(decltype(s_c)::value, s_c); });
-    for (int t0 = 0; t0 < ntr; t0 += DEPTH) {
-        static_for<DEPTH>([&](auto s_c) {
-            __builtin_amdgcn_s_waitcnt(kWaitOldest);
-            compute(s_c);
-            __builtin_amdgcn_s_waitcnt(kWaitLds);     // the stage's A reads are done before its refill
-            issue(t0 + decltype(s_c)::value + DEPTH, s_c);
-        });
+    auto stream = [&]() {
+        static_for<DEPTH>([&](auto s_c) { issue(decltype(s_c)::value, s_c); });
+        for (int t0 = 0; t0 < ntr; t0 += DEPTH) {
+            static_for<DEPTH>([&](auto s_c) {
+                __builtin_amdgcn_s_waitcnt(kWaitOldest);
+                compute(s_c);
+                __builtin_amdgcn_s_waitcnt(kWaitLds);     // the stage's A reads are done before its refill
+                issue(t0 + decltype(s_c)::value + DEPTH, s_c);
+            });
+        }
+    };
+    if constexpr (LORA) {
+        if (w < WAVES)
+            stream();
+        else
+            lora_skinny<MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
+    } else {
+        stream();
     }
     __builtin_amdgcn_s_waitcnt(kWaitVmcnt0 & ~0x0F00);
     if constexpr (MX)
         mfma_drain_acc(acc);                      // the scaled MFMAs are inline assembly
     __syncthreads();
-    skinny_finish<MB, OUT, WAVES, ELEM == kI8 ? 1 : (W4 ? 16 : 0), EX>(p, acc, lds, n0);
+    skinny_finish<MB, OUT, skinny_waves<WAVES, LORA>(), ELEM == kI8 ? 1 : (W4 ? 16 : 0), EX>(p, acc, lds, n0);
 }
 
-template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX = false>
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD, bool EX = false, bool LORA = false>
 static hipError_t launch_skinny_pre(const SkinnyArgs &a, int grid, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_skinny_pre_kernel<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, EX>), dim3(grid), dim3(64 * WAVES), 0,
-                       s, a);
+    hipLaunchKernelGGL((gemm_skinny_pre_kernel<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, EX, LORA>), dim3(grid),
+                       dim3(64 * skinny_waves<WAVES, LORA>()), 0, s, a);
     return hipGetLastError();
+}
+template <int MB, int ELEM, int OUT, int WAVES, int DEPTH, bool BLDS, int ORD>
+constexpr SkinnyLaunch skinny_pre_lora()
+{
+    if constexpr (ELEM == kBf16)
+        return &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, true, true>;
+    else
+        return nullptr;
 }
 
 #define TG_SKINNY(MB, ELEM, OUT, WAVES, DEPTH, ROTATE)                                                       \
     SkinnyVariant{MB, ELEM, OUT, WAVES, DEPTH, SkinnyCfg<MB, WAVES, DEPTH>::LDS,                             \
                   &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE>, false,                                \
-                  &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, true>}
+                  &launch_skinny<MB, ELEM, OUT, WAVES, DEPTH, ROTATE, true>,                                 \
+                  skinny_lora<MB, ELEM, OUT, WAVES, DEPTH, ROTATE>()}
 
 #define TG_SKINNY_PRE_O(MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD)                                              \
     SkinnyVariant{MB, ELEM, OUT, WAVES, DEPTH, SkinnyPreCfg<MB, WAVES, DEPTH, BLDS, ELEM == kW4A8 ? 1 : 2>::LDS, \
                   &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD>, true,                           \
-                  &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, true>}
+                  &launch_skinny_pre<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD, true>,                           \
+                  skinny_pre_lora<MB, ELEM, OUT, WAVES, DEPTH, BLDS, ORD>()}
 #define TG_SKINNY_PRE_L(MB, ELEM, OUT, WAVES, DEPTH, BLDS) TG_SKINNY_PRE_O(MB, ELEM, OUT, WAVES, DEPTH, BLDS, 1)
 #define TG_SKINNY_PRE(MB, ELEM, OUT, WAVES, DEPTH) TG_SKINNY_PRE_L(MB, ELEM, OUT, WAVES, DEPTH, false)
 

@@ -34,6 +34,7 @@
 //     and lane i of the block ends up with rows k0 .. k0 + 3 of column
 //     c0 + i.  Rows past K lie past the end of B and read as zeros.
 #include "group.hpp"
+#include "lora.hpp"
 
 namespace tg {
 
@@ -67,7 +68,8 @@ struct TiledCfg {
     static_assert(LDS <= 160 * 1024, "gfx950 LDS is 160 KiB per workgroup");
 };
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false, int NS = 2>
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false, int NS = 2,
+          bool LORA = false>
 __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p0)
 {
     TiledArgs p = p0;
@@ -335,6 +337,8 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
     const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
+    if constexpr (LORA)
+        lora_tail<FM, FN>(p.lora, acc, m0, rows_a, wm * Cfg::WTM, n0 + wn * Cfg::WTN, p.N);
     if constexpr (EX) {
         constexpr int EB = Cfg::EB;
         __syncthreads();                       // every wave has read its last fragments before LDS is reused
@@ -366,12 +370,23 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX = false>
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX = false, int NS = 2,
+          bool LORA = false>
 static hipError_t launch_tiled(const TiledArgs &a, hipStream_t s)
 {
-    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, EX>), dim3(a.grid),
+    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, EX, false, NS, LORA>), dim3(a.grid),
                        dim3(kTiledThreads), 0, s, a);
     return hipGetLastError();
+}
+using TiledLaunch = hipError_t (*)(const TiledArgs &, hipStream_t);
+// The kernel behind low-rank adapters: bf16, B N x K or pre-shuffled.
+template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, int NS>
+constexpr TiledLaunch tiled_lora()
+{
+    if constexpr (ELEM == kBf16 && !BKN)
+        return &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, true, NS, true>;
+    else
+        return nullptr;
 }
 
 #define TG_TILED_L(BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN)                                 \
@@ -383,7 +398,8 @@ static hipError_t launch_tiled(const TiledArgs &a, hipStream_t s)
     TiledVariant{BM, BN, WGM, WGN, ELEM, OUT, BPRE,                                         \
                  TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>::LDS, 2,                  \
                  &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN>, BKN, false,          \
-                 &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, true>}
+                 &launch_tiled<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, true>,                \
+                 tiled_lora<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, 2>()}
 #define TG_TILED(BM, BN, WGM, WGN, ELEM, BPRE, OUT) TG_TILED_L(BM, BN, WGM, WGN, ELEM, BPRE, OUT, false)
 
 static const TiledVariant kTiled[] = {
@@ -438,16 +454,10 @@ const GroupVariant *group_tiled_variants(int *count)
 
 // The extended epilogue on smaller tiles with a ring of stages, for grids
 // that leave CUs idle (plan_ex in capi.cpp), small tiles first.
-template <int BM, int BN, int NS, int ELEM, bool BPRE, int OUT, bool BKN>
-static hipError_t launch_small(const TiledArgs &a, hipStream_t s)
-{
-    hipLaunchKernelGGL((gemm_tiled_kernel<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, true, false, NS>), dim3(a.grid),
-                       dim3(kTiledThreads), 0, s, a);
-    return hipGetLastError();
-}
 #define TG_SMALL(BM, BN, NS, ELEM, BPRE, OUT, BKN)                                         \
     TiledVariant{BM, BN, 2, 2, ELEM, OUT, BPRE, TiledCfg<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, NS>::LDS, NS, \
-                 nullptr, BKN, false, &launch_small<BM, BN, NS, ELEM, BPRE, OUT, BKN>}
+                 nullptr, BKN, false, &launch_tiled<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, true, NS>,        \
+                 tiled_lora<BM, BN, 2, 2, ELEM, BPRE, OUT, BKN, NS>()}
 #define TG_SMALL_ALL(BM, BN, NS)                                                           \
     TG_SMALL(BM, BN, NS, kBf16, false, kOutBf16, false), TG_SMALL(BM, BN, NS, kBf16, false, kOutF32, false), \
     TG_SMALL(BM, BN, NS, kBf16, true, kOutBf16, false),  TG_SMALL(BM, BN, NS, kBf16, true, kOutF32, false),  \

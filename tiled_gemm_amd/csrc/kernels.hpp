@@ -39,6 +39,24 @@ struct GroupArgs {
     int64_t b_stride;           // bytes from one group's B to the next
 };
 
+// Low-rank adapters beside the projection (lora.hpp, lora.hip).
+struct LoraArgs {
+    const int32_t *adapter;     // M: the adapter of each row (outside 0 .. adapters - 1: none)
+    const float *v;             // workspace: parts x M x rank_pad
+    float *v_out;               // the same, to the kernel that writes it
+    const void *x;              // M x K bf16
+    const void *down;           // adapters x rank x K bf16
+    const void *up;             // adapters x N x rank bf16
+    const float *scale;         // nullptr (1) or one per adapter
+    int32_t adapters, rank;
+    int32_t rank_pad;           // rank rounded up to 32 (the rest of v is zeros)
+    int32_t M, K;
+    int32_t parts;              // partial sums over K
+};
+// Rows up to which the first half works on one adapter per workgroup.
+constexpr int kLoraFewRows = 128;
+hipError_t launch_lora_down(const LoraArgs &, hipStream_t);
+
 struct TiledArgs {
     const void *A;
     const void *B;
@@ -66,6 +84,7 @@ struct TiledArgs {
     int32_t splits;
     int32_t split_steps;
     GroupArgs grp;
+    LoraArgs lora;          // launch_lora, launch_lora_part
 };
 
 // Sum of the split-K partials and the epilogue: C[m][n] = cvt(epi(sum over
@@ -117,6 +136,7 @@ struct SkinnyArgs {
     const uint8_t *sa_img;
     const uint8_t *sb_img;
     int32_t s_groups;
+    LoraArgs lora;          // launch_lora
 };
 
 struct PreshuffleArgs {
@@ -141,6 +161,11 @@ struct TiledVariant {
     // The kernel with the extended epilogue (residual, saved pre-activation):
     // present for every variant a plan with the planner's own choice can get.
     hipError_t (*launch_ex)(const TiledArgs &, hipStream_t) = nullptr;
+    // bf16 with B N x K or pre-shuffled: the extended epilogue behind low-rank
+    // adapters; and (fp32 output) the split-K partial tiles, the first slice
+    // with them.
+    hipError_t (*launch_lora)(const TiledArgs &, hipStream_t) = nullptr;
+    hipError_t (*launch_lora_part)(const TiledArgs &, hipStream_t) = nullptr;
 };
 
 struct SkinnyVariant {
@@ -152,6 +177,7 @@ struct SkinnyVariant {
     hipError_t (*launch)(const SkinnyArgs &, int grid, hipStream_t);
     bool preshuffled = false;   // B is the pre-shuffled image (register-staged B)
     hipError_t (*launch_ex)(const SkinnyArgs &, int grid, hipStream_t) = nullptr;   // extended epilogue
+    hipError_t (*launch_lora)(const SkinnyArgs &, int grid, hipStream_t) = nullptr; // and low-rank adapters (bf16)
 };
 
 // A grouped kernel (group.hpp): tiles of bm x bn.
@@ -226,7 +252,6 @@ hipError_t launch_ckpt_unpack(const CkptArgs &, hipStream_t);
 constexpr int kMlpTokens = 64;
 constexpr int kMlpTopk = 64;
 constexpr int kMlpSlots = kMlpTokens * kMlpTopk;
-constexpr int kMlpTileN = 32;               // weight rows of one work item
 constexpr int kMlpGrid = 512;               // two workgroups per CU
 struct MlpArgs {
     const void *x;                          // tokens x K bf16

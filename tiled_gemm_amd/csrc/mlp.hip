@@ -19,15 +19,14 @@
 //     writes its slots' fp32 sums, and the workgroup that finishes a column tile
 //     last adds the slots of every token in the order of j.  Which workgroup that
 //     is does not change the result.
-#include "cols.hpp"
+#include "stream.hpp"
 
 namespace tg {
 
 namespace {
 
-constexpr int kMlpWaves = 8;
-constexpr int kMlpThreads = 64 * kMlpWaves;
-constexpr int kMlpPitch = kMlpTileN + 1;
+constexpr int kMlpThreads = kStreamThreads;
+constexpr int kMlpPitch = stream_pitch<2>();
 constexpr int kMlpBits = kMaxGroups / 32;          // words of the bitmap of experts
 static_assert(kMlpBits == 32, "one word per lane of half a wave");
 
@@ -103,99 +102,6 @@ __device__ inline int mlp_rows(MlpShared &sh, int slots, int e)
     return __builtin_amdgcn_readfirstlane(sh.cnt);
 }
 
-// Eight e4m3 elements (two words) as an MFMA operand of eight bf16: exact.
-__device__ inline u32x4 fp8x8_to_bf16(uint32_t lo, uint32_t hi)
-{
-    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.f, true);
-    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, false);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.f, true);
-    return u32x4{__builtin_bit_cast(uint32_t, a), __builtin_bit_cast(uint32_t, b), __builtin_bit_cast(uint32_t, c),
-                 __builtin_bit_cast(uint32_t, d)};
-}
-
-// Products of up to 16 MB gathered rows with two blocks of 16 weight rows, K
-// split over the waves; the waves' sums end up in red, to be added over w.
-//   rX      the rows' array; xoff[i]: byte offset of this lane's row (l % 16 of
-//           row block i), past the array for rows that are not there
-//   rB[j]   weight block j: 16 rows of kb bytes (or their image)
-// A step is 64 bytes of K of the weights: lane 16 q + r holds bytes 16 q .. of row
-// r, one MFMA of bf16 or two of e4m3 (elements 16 q .. + 7 and + 8 .. + 15).
-template <int MB, bool E8, bool PRE, int U>
-__device__ inline void mlp_product(__amdgpu_buffer_rsrc_t rX, const uint32_t (&xoff)[MB],
-                                   const __amdgpu_buffer_rsrc_t (&rB)[2], uint32_t kb, float (*red)[16 * MB][kMlpPitch])
-{
-    constexpr int H = E8 ? 2 : 1;                    // MFMAs (and 16-byte loads of a row of x) per step
-    const int w = wave_id(), l = lane_id(), q = l >> 4, r16 = l & 15;
-    const int steps = (int)(kb / 64), per = (steps + kMlpWaves - 1) / kMlpWaves;
-    const int first = w * per, nt = max(0, min(per, steps - first));
-    const uint32_t boff = PRE ? (uint32_t)l * 16u : (uint32_t)r16 * kb + (uint32_t)q * 16u;
-    struct Set {
-        u32x4 b[U][2];
-        u32x4 x[U][MB][H];
-    };
-    auto load = [&](int t0, Set &s) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool in = t0 + u < nt;
-            const uint32_t k = in ? (uint32_t)(first + t0 + u) : 0u;
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                s.b[u][j] = buf_load16(rB[j], keep_or_oob(in, boff), k * (PRE ? 1024u : 64u));
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-#pragma unroll
-                for (int h = 0; h < H; ++h)
-                    s.x[u][i][h] = buf_load16(rX, keep_or_oob(in, xoff[i] + (uint32_t)(q * 16 * H + 16 * h)),
-                                              k * (64u * H));
-        }
-        issue_fence();
-    };
-    f32x4 acc[MB][2];
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-        acc[i][0] = acc[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto compute = [&](const Set &s) {
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const u32x4 b = E8 ? fp8x8_to_bf16(s.b[u][j][2 * h], s.b[u][j][2 * h + (E8 ? 1 : 0)]) : s.b[u][j];
-#pragma unroll
-                    for (int i = 0; i < MB; ++i)
-                        acc[i][j] = mfma_bf16(b, s.x[u][i][h], acc[i][j]);
-                }
-    };
-    Set s0, s1;
-    load(0, s0);
-    for (int t = 0; t < nt; t += 2 * U) {
-        load(t + U, s1);
-        compute(s0);
-        load(t + 2 * U, s0);
-        compute(s1);
-    }
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int v = 0; v < 4; ++v)
-                red[w][i * 16 + r16][j * 16 + 4 * q + v] = acc[i][j][v];
-}
-
-template <int MB>
-__device__ inline float mlp_sum(const float (*red)[16 * MB][kMlpPitch], int row, int col)
-{
-    float s = 0.f;
-#pragma unroll
-    for (int w = 0; w < kMlpWaves; ++w)
-        s += red[w][row][col];
-    return s;
-}
-
 }  // namespace
 
 // x -> h.  Column tile c: the gate's and the linear half's columns 16 c .. + 15
@@ -218,7 +124,7 @@ __device__ inline void mlp_up_item(const MlpArgs &a, const MlpShared &sh, int e,
         const int r = r0 + i * 16 + r16;
         xoff[i] = keep_or_oob(r < cnt, (uint32_t)(sh.rows[r < cnt ? r : 0] / a.topk) * (uint32_t)a.K * 2u);
     }
-    mlp_product<MB, E8, PRE, U>(rX, xoff, rB, kb, red);
+    stream_product<MB, 2, E8, PRE, U>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
     __syncthreads();
     const int cols = a.gated ? 16 : 32;
     for (int o = threadIdx.x; o < 16 * MB * cols; o += kMlpThreads) {
@@ -227,14 +133,14 @@ __device__ inline void mlp_up_item(const MlpArgs &a, const MlpShared &sh, int e,
         if (r0 + row >= cnt)
             continue;
         const size_t at = (size_t)e * inner + n;
-        float z = mlp_sum<MB>(red, row, col);
+        float z = stream_sum<MB, 2>(red, row, col);
         if (a.up_scale)
             z *= a.up_scale[at];
         if (a.up_bias)
             z += a.up_bias[at];
         float y = a.act == kActSilu ? epi_silu(z) : epi_act(z, a.act);
         if (a.gated) {
-            float u = mlp_sum<MB>(red, row, 16 + col);
+            float u = stream_sum<MB, 2>(red, row, 16 + col);
             if (a.up_scale)
                 u *= a.up_scale[at + a.N];
             if (a.up_bias)
@@ -251,7 +157,7 @@ template <int MB, bool E8, bool PRE>
 __global__ __launch_bounds__(kMlpThreads, 4) void mlp_up_kernel(const MlpArgs a)
 {
     __shared__ MlpShared sh;
-    __shared__ float lds[kMlpWaves * 16 * MB * kMlpPitch];
+    __shared__ float lds[kStreamWaves * 16 * MB * kMlpPitch];
     constexpr int U = E8 ? 2 : 4;
     if (blockIdx.x == 0)
         for (int c = threadIdx.x; c < a.down_tiles; c += kMlpThreads)
@@ -293,14 +199,14 @@ __device__ inline void mlp_down_item(const MlpArgs &a, const MlpShared &sh, int 
         const int r = r0 + i * 16 + r16;
         xoff[i] = keep_or_oob(r < cnt, (uint32_t)sh.rows[r < cnt ? r : 0] * (uint32_t)a.N * 2u);
     }
-    mlp_product<MB, E8, PRE, U>(rX, xoff, rB, kb, red);
+    stream_product<MB, 2, E8, PRE, U>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
     __syncthreads();
     for (int o = threadIdx.x; o < 16 * MB * 32; o += kMlpThreads) {
         const int row = o / 32, n = n0 + o % 32;
         if (r0 + row >= cnt)
             continue;
         const size_t at = (size_t)e * a.K + n;
-        float z = mlp_sum<MB>(red, row, o % 32);
+        float z = stream_sum<MB, 2>(red, row, o % 32);
         if (a.down_scale)
             z *= a.down_scale[at];
         if (a.down_bias)
@@ -313,7 +219,7 @@ template <int MB, bool E8, bool PRE>
 __global__ __launch_bounds__(kMlpThreads, 4) void mlp_down_kernel(const MlpArgs a)
 {
     __shared__ MlpShared sh;
-    __shared__ float lds[kMlpWaves * 16 * MB * kMlpPitch];
+    __shared__ float lds[kStreamWaves * 16 * MB * kMlpPitch];
     constexpr int U = E8 ? 2 : 4;
     // Without any active expert the column tiles still have to be written.
     const int active = mlp_mark(sh, a), parts = max(active, 1), items = parts * a.down_tiles;
