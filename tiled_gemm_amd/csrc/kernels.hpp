@@ -42,8 +42,11 @@ struct GroupArgs {
 // Low-rank adapters beside the projection (lora.hpp, lora.hip).
 struct LoraArgs {
     const int32_t *adapter;     // M: the adapter of each row (outside 0 .. adapters - 1: none)
-    const float *v;             // workspace: parts x M x rank_pad
-    float *v_out;               // the same, to the kernel that writes it
+    // Workspace.  planes: M x rank_pad bf16 twice, v = the first + the second
+    // (the tile kernels).  Otherwise parts x M x rank_pad fp32, v their sum
+    // (the skinny kernels).
+    void *v;
+    bool planes;
     const void *x;              // M x K bf16
     const void *down;           // adapters x rank x K bf16
     const void *up;             // adapters x N x rank bf16
@@ -51,10 +54,12 @@ struct LoraArgs {
     int32_t adapters, rank;
     int32_t rank_pad;           // rank rounded up to 32 (the rest of v is zeros)
     int32_t M, K;
-    int32_t parts;              // partial sums over K
+    int32_t parts;              // partial sums over K (planes: 1)
 };
-// Rows up to which the first half works on one adapter per workgroup.
+// Rows up to which the first half works on one adapter per workgroup, and the
+// most parts of K.
 constexpr int kLoraFewRows = 128;
+constexpr int kLoraParts = 4;
 hipError_t launch_lora_down(const LoraArgs &, hipStream_t);
 
 struct TiledArgs {

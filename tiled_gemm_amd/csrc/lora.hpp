@@ -10,11 +10,11 @@
 // (Choosing the finished sums rather than clearing the other rows' v keeps an
 // infinity or NaN of one adapter's matrices out of the other adapters' rows.)
 //
-// v comes as fp32 (in `parts` partial sums over K) and goes to the matrix unit
-// as two bf16 numbers, v = hi + lo within 2^-17 of it, for twice the MFMAs of a
-// product that is 1 to 3% of the projection's: rounding v to one bf16 would add
-// an error as large as the output's own rounding where the adapters' share of z
-// is large.
+// v goes to the matrix unit as two bf16 numbers, v = hi + lo within 2^-17 of it,
+// for twice the MFMAs of a product that is 1 to 3% of the projection's: rounding
+// v to one bf16 would add an error as large as the output's own rounding where
+// the adapters' share of z is large.  The tile kernels read hi and lo; the skinny
+// kernels, whose v is made in parts of K, read fp32 partial sums.
 #pragma once
 
 #include "device.hpp"
@@ -32,72 +32,58 @@ __device__ inline void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 &hi, u32
     }
 }
 
-// acc += v up_e^T for the rows whose bit is set in `same` (bit 16 i + r: row r of
-// block i).  row[i]: this lane's row of block i within the tile; col0: the wave's
-// first column.
-template <int CH, int FN>
-__device__ inline void lora_add(const LoraArgs &lo, int m0, int rows, int N, f32x4 (*acc)[FN], const int (&row)[CH],
-                                unsigned long long same, int e, int col0)
-{
-    const int l = lane_id(), q = l >> 4, r16 = l & 15;
-    const uint32_t pitch = (uint32_t)lo.rank_pad * 4u, upitch = (uint32_t)lo.rank * 2u;
-    const auto ru = make_rsrc((const uint8_t *)lo.up + (size_t)e * (size_t)N * upitch, (uint32_t)N * upitch);
-    f32x4 t[CH][FN];
-#pragma unroll
-    for (int i = 0; i < CH; ++i)
-#pragma unroll
-        for (int j = 0; j < FN; ++j)
-            t[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-    for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
-        u32x4 b[FN];
+// This lane's place among the columns of `up`: its row r16 of each column block
+// and the 8 ranks from r0 + 8 q, as byte offsets (past the matrix for columns
+// past N and ranks past the last).
+template <int FN>
+struct LoraCols {
+    uint32_t off[FN];
+    uint32_t bytes;              // of one adapter's matrix
+    __device__ LoraCols(const LoraArgs &lo, int N, int col0, int r0)
+    {
+        const int l = lane_id(), r = r0 + 8 * (l >> 4);
+        const uint32_t pitch = (uint32_t)lo.rank * 2u;
+        bytes = (uint32_t)N * pitch;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            const int col = col0 + j * 16 + r16;
-            b[j] = buf_load16(ru, keep_or_oob(col < N && r0 + 8 * q < lo.rank,
-                                              (uint32_t)col * upitch + (uint32_t)(r0 + 8 * q) * 2u), 0);
-        }
-        f32x4 va[CH], vb[CH];
-#pragma unroll
-        for (int i = 0; i < CH; ++i)
-            va[i] = vb[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        for (int s = 0; s < lo.parts; ++s) {
-            const auto rv = make_rsrc(lo.v + ((size_t)s * lo.M + m0) * lo.rank_pad, (uint32_t)rows * pitch);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const uint32_t off = keep_or_oob(row[i] < rows, (uint32_t)row[i] * pitch + (uint32_t)(r0 + 8 * q) * 4u);
-                va[i] += __builtin_bit_cast(f32x4, buf_load16(rv, off, 0));
-                vb[i] += __builtin_bit_cast(f32x4, buf_load16(rv, off, 16));
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) {
-            u32x4 hi, low;
-            split_bf16(va[i], vb[i], hi, low);
-#pragma unroll
-            for (int j = 0; j < FN; ++j) {
-                t[i][j] = mfma_bf16(b[j], hi, t[i][j]);
-                t[i][j] = mfma_bf16(b[j], low, t[i][j]);
-            }
+            const int col = col0 + j * 16 + (l & 15);
+            off[j] = keep_or_oob(col < N && r < lo.rank, (uint32_t)col * pitch + (uint32_t)r * 2u);
         }
     }
+    __device__ void load(const LoraArgs &lo, int e, u32x4 (&b)[FN]) const
+    {
+        const auto ru = make_rsrc((const uint8_t *)lo.up + (size_t)e * bytes, bytes);
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+            b[j] = buf_load16(ru, off[j], 0);
+    }
+};
+
+// acc += v b^T for the rows whose bit is set in `same` (bit 16 i + r: row r of
+// block i), 32 ranks.
+template <int CH, int FN>
+__device__ inline void lora_add(f32x4 (*acc)[FN], const u32x4 (&hi)[CH], const u32x4 (&lo)[CH], const u32x4 (&b)[FN],
+                                unsigned long long same)
+{
+    const int r16 = lane_id() & 15;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
         const bool mine = (same >> (i * 16 + r16)) & 1;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j) {
+            f32x4 t = mfma_bf16(b[j], hi[i], f32x4{0.f, 0.f, 0.f, 0.f});
+            t = mfma_bf16(b[j], lo[i], t);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                acc[i][j][c] += mine ? t[i][j][c] : 0.f;
+                acc[i][j][c] += mine ? t[c] : 0.f;
+        }
     }
 }
 
-// The adapters of a wave's CH row blocks, one row per lane (-1: none); the lane
-// of row r of block i is 16 i + r.
-template <int CH>
-__device__ inline int lora_ids(const LoraArgs &lo, int m0, int rows, int first_row)
+// The adapter of one row per lane (-1: none).
+__device__ inline int lora_id(const LoraArgs &lo, bool there, int row)
 {
-    const int l = lane_id(), row = first_row + l;
-    const int id = l < 16 * CH && row < rows ? lo.adapter[m0 + row] : -1;
+    const int id = there ? lo.adapter[row] : -1;
     return (uint32_t)id < (uint32_t)lo.adapters ? id : -1;
 }
 
@@ -106,24 +92,50 @@ __device__ inline int lora_ids(const LoraArgs &lo, int m0, int rows, int first_r
 template <int FM, int FN>
 __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], int m0, int rows, int row0, int col0, int N)
 {
-    // Row blocks at a time: as many sums beside the accumulators as still
-    // leave registers for the operands.
-    constexpr int CH = FN >= 4 ? 2 : (FM < 4 ? FM : 4);
+    constexpr int CH = FM < 4 ? FM : 4;              // row blocks at a time: a row per lane
+    constexpr int CHUNKS = FM / CH;
     static_assert(FM % CH == 0, "whole chunks");
-    static_for<FM / CH>([&](auto c_c) {
-        constexpr int C = decltype(c_c)::value * CH;
-        const int id = lora_ids<CH>(lo, m0, rows, row0 + 16 * C);
-        int row[CH];
+    const int l = lane_id(), q = l >> 4, r16 = l & 15;
+    const uint32_t pitch = (uint32_t)lo.rank_pad * 2u;
+    const uint8_t *const hi0 = (const uint8_t *)lo.v + (size_t)m0 * pitch;
+    const auto rh = make_rsrc(hi0, (uint32_t)rows * pitch);
+    const auto rl = make_rsrc(hi0 + (size_t)lo.M * pitch, (uint32_t)rows * pitch);
+    int id[CHUNKS];
 #pragma unroll
-        for (int i = 0; i < CH; ++i)
-            row[i] = row0 + 16 * (C + i) + (lane_id() & 15);
-        for (unsigned long long left = __ballot(id >= 0); left;) {
-            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-            const unsigned long long same = __ballot(id == e);
-            left &= ~same;
-            lora_add<CH, FN>(lo, m0, rows, N, &acc[C], row, same, e, col0);
-        }
-    });
+    for (int c = 0; c < CHUNKS; ++c) {
+        const int row = row0 + 16 * CH * c + l;
+        id[c] = lora_id(lo, l < 16 * CH && row < rows, m0 + row);
+    }
+    const uint32_t off = (uint32_t)(row0 + r16) * pitch + (uint32_t)(8 * q) * 2u;
+    for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
+        const LoraCols<FN> cols(lo, N, col0, r0);
+        u32x4 b[FN];
+        int have = -1;                               // the adapter whose columns b holds
+        static_for<CHUNKS>([&](auto c_c) {
+            constexpr int C = decltype(c_c)::value;
+            unsigned long long left = __ballot(id[C] >= 0);
+            if (!left)
+                return;
+            u32x4 hi[CH], low[CH];
+#pragma unroll
+            for (int i = 0; i < CH; ++i) {
+                // rows past the tile's last are past the record count
+                const uint32_t at = off + (uint32_t)(16 * (C * CH + i)) * pitch + (uint32_t)r0 * 2u;
+                hi[i] = buf_load16(rh, at, 0);
+                low[i] = buf_load16(rl, at, 0);
+            }
+            while (left) {
+                const int e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
+                const unsigned long long same = __ballot(id[C] == e);
+                left &= ~same;
+                if (e != have) {
+                    cols.load(lo, e, b);
+                    have = e;
+                }
+                lora_add<CH, FN>(&acc[C * CH], hi, low, b, same);
+            }
+        });
+    }
 }
 
 // The same for a few rows (M <= 64), the adapters shared out to `waves` waves:
@@ -132,18 +144,58 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], int m
 template <int MB, int FN>
 __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int M, int N, int col0, int w, int waves)
 {
-    const int id = lora_ids<MB>(lo, 0, M, 0);
-    int row[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i)
-        row[i] = 16 * i + (lane_id() & 15);
+    const int l = lane_id(), q = l >> 4, r16 = l & 15;
+    const int id = lora_id(lo, l < M, l);
+    const uint32_t pitch = (uint32_t)lo.rank_pad * 4u;
+    const auto rv = make_rsrc(lo.v, (uint32_t)(lo.parts * M) * pitch);
+    // The wave's next adapter: its first row's, every waves-th of those left.
+    unsigned long long left = 0;
     int n = 0;
-    for (unsigned long long left = __ballot(id >= 0); left; ++n) {
-        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        const unsigned long long same = __ballot(id == e);
-        left &= ~same;
-        if (n % waves == w)
-            lora_add<MB, FN>(lo, 0, M, N, acc, row, same, e, col0);
+    auto next = [&](unsigned long long *same) {
+        while (left) {
+            const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+            *same = __ballot(id == e);
+            left &= ~*same;
+            if (n++ % waves == w)
+                return e;
+        }
+        return -1;
+    };
+    for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
+        const LoraCols<FN> cols(lo, N, col0, r0);
+        left = __ballot(id >= 0);
+        n = 0;
+        unsigned long long same = 0, same1 = 0;
+        int e = next(&same);
+        if (e < 0)
+            return;                                  // fewer adapters than waves
+        u32x4 b[FN], b1[FN];
+        cols.load(lo, e, b);
+        u32x4 hi[MB], low[MB];
+#pragma unroll
+        for (int i = 0; i < MB; ++i) {
+            const int row = 16 * i + r16;
+            f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
+#pragma unroll
+            for (int s = 0; s < kLoraParts; ++s) {
+                const uint32_t at = keep_or_oob(row < M && s < lo.parts,
+                                                (uint32_t)(s * M + row) * pitch + (uint32_t)(r0 + 8 * q) * 4u);
+                va += __builtin_bit_cast(f32x4, buf_load16(rv, at, 0));
+                vb += __builtin_bit_cast(f32x4, buf_load16(rv, at, 16));
+            }
+            split_bf16(va, vb, hi[i], low[i]);
+        }
+        while (e >= 0) {
+            const int e1 = next(&same1);
+            if (e1 >= 0)
+                cols.load(lo, e1, b1);               // in flight while this one's products run
+            lora_add<MB, FN>(acc, hi, low, b, same);
+            e = e1;
+            same = same1;
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+                b[j] = b1[j];
+        }
     }
 }
 
