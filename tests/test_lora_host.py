@@ -70,7 +70,7 @@ def test_workspace():
         assert p.lora_workspace_bytes(16) == pad(4 * 7 * 32 * 4)
     with tg.Plan(256, 4096, 8192, BF, PRE) as p:               # partial tiles behind v
         assert p.workspace_bytes() > 0
-        assert p.lora_workspace_bytes(32) == pad(256 * 32 * 4) + p.workspace_bytes()
+        assert p.lora_workspace_bytes(32) == pad(4 * 256 * 32 * 4) + p.workspace_bytes()
     with tg.Plan(0, 64, 128, BF, BT) as p:
         assert p.lora_workspace_bytes(16) == 0
         run(p, A=0, B=0, C=0, adapter=0, down=0, up=0, scale=0, residual=0, preact=0, workspace=0)      # nothing to do

@@ -959,20 +959,9 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
     return GEMM_OK;
 }
 
-// K is shared out over this many workgroups in the adapters' first half, where
-// each has one adapter and the skinny kernels add the parts: 64 KiB of 16 ranks
-// each (32 x 8192 x 8192, 24 adapters of rank 16: PARTS_MEASURED).
-int lora_parts(const gemm_plan *plan)
-{
-    if (plan->info.kernel != 1)
-        return 1;
-    const int64_t p = (plan->info.K * 2 * 16 + (64 << 10) - 1) / (64 << 10);
-    return (int)(p < 1 ? 1 : p > tg::kLoraParts ? tg::kLoraParts : p);
-}
-
 size_t lora_v_bytes(const gemm_plan *plan, int rank)
 {
-    const size_t n = (size_t)lora_parts(plan) * (size_t)plan->info.M * (size_t)((rank + 31) / 32 * 32) * 4;
+    const size_t n = (size_t)tg::lora_parts(plan->info.M, plan->info.K) * (size_t)plan->info.M * (size_t)((rank + 31) / 32 * 32) * 4;
     return (n + 255) / 256 * 256;
 }
 
@@ -1137,8 +1126,7 @@ int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, 
         return rc;
     tg::LoraArgs l{};
     l.adapter = lora->adapter;
-    l.v = workspace;
-    l.planes = I.kernel != 1;
+    l.v = (float *)workspace;
     l.x = A;
     l.down = lora->down;
     l.up = lora->up;
@@ -1148,7 +1136,7 @@ int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, 
     l.rank_pad = (lora->rank + 31) / 32 * 32;
     l.M = (int32_t)I.M;
     l.K = (int32_t)I.K;
-    l.parts = lora_parts(plan);
+    l.parts = tg::lora_parts(I.M, I.K);
     const hipError_t r = tg::launch_lora_down(l, stream);
     if (r != hipSuccess)
         return fail(GEMM_ERR_HIP, "adapters' launch: %s", hipGetErrorString(r));

@@ -337,8 +337,9 @@ __global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const Tile
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
     const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
+    static_assert(!LORA || lora_lds_bytes<BM>() <= Cfg::LDS, "v fits the stages");
     if constexpr (LORA)
-        lora_tail<FM, FN>(p.lora, acc, m0, rows_a, wm * Cfg::WTM, n0 + wn * Cfg::WTN, p.N);
+        lora_tail<BM, kTiledThreads>(p.lora, acc, lds, m0, rows_a, wm * Cfg::WTM, n0 + wn * Cfg::WTN, p.N);
     if constexpr (EX) {
         constexpr int EB = Cfg::EB;
         __syncthreads();                       // every wave has read its last fragments before LDS is reused

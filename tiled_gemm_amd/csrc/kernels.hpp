@@ -42,11 +42,7 @@ struct GroupArgs {
 // Low-rank adapters beside the projection (lora.hpp, lora.hip).
 struct LoraArgs {
     const int32_t *adapter;     // M: the adapter of each row (outside 0 .. adapters - 1: none)
-    // Workspace.  planes: M x rank_pad bf16 twice, v = the first + the second
-    // (the tile kernels).  Otherwise parts x M x rank_pad fp32, v their sum
-    // (the skinny kernels).
-    void *v;
-    bool planes;
+    float *v;                   // workspace: parts x M x rank_pad
     const void *x;              // M x K bf16
     const void *down;           // adapters x rank x K bf16
     const void *up;             // adapters x N x rank bf16
@@ -54,12 +50,10 @@ struct LoraArgs {
     int32_t adapters, rank;
     int32_t rank_pad;           // rank rounded up to 32 (the rest of v is zeros)
     int32_t M, K;
-    int32_t parts;              // partial sums over K (planes: 1)
+    int32_t parts;              // partial sums over K, lora_parts(M, K)
 };
-// Rows up to which the first half works on one adapter per workgroup, and the
-// most parts of K.
-constexpr int kLoraFewRows = 128;
 constexpr int kLoraParts = 4;
+int lora_parts(int64_t M, int64_t K);
 hipError_t launch_lora_down(const LoraArgs &, hipStream_t);
 
 struct TiledArgs {

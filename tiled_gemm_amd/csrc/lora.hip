@@ -2,17 +2,20 @@
 //
 //   v[m][r] = s_a sum_k x[m][k] down_a[r][k],     a the adapter of row m
 //
-// for the projection's kernel to finish (lora.hpp), as fp32 or as two bf16
-// numbers.  Two forms, by the number of rows:
-//   * up to kLoraFewRows (decode): the adapters' matrices are the bytes, most
-//     rows have one of their own, and a workgroup alone would take long over
-//     one.  So a workgroup takes one adapter of 16 rows, 16 of its ranks and one
-//     part of K.
+// for the projection's kernel to finish (lora.hpp): fp32 sums over parts of K.
+//
+// A CU alone streams some 30 to 50 GB/s, so what counts is the bytes that each
+// workgroup reads and that there are enough workgroups: K is cut into parts (up
+// to kLoraParts), which the reader adds.  Two forms, by the number of rows:
+//   * up to kFewRows (decode): the adapters' matrices are the bytes, most rows
+//     have one of their own.  A workgroup takes one adapter of 16 rows, 16 of its
+//     ranks and one part.
 //   * above (prompts, training): x is the bytes, and blocks of rows mostly have
-//     one adapter.  A workgroup takes the first adapter of 16 or 32 rows with up
-//     to 64 ranks at once, x read once for them.  The further adapters of a
-//     group of 64 rows (decode rows in front of the prompts, a prompt's end) are
-//     shared out to kLoraMore workgroups more: one after the other in the
+//     one adapter.  A workgroup takes the first adapter of 16, 32 or 64 rows (so
+//     many that the parts still give every CU one) with up to 64 ranks at once,
+//     x read once for them.  The further adapters of a block (decode rows in
+//     front of the prompts, a prompt's end) are shared out to kMore workgroups
+//     more, which read the rows of theirs only.  One after the other in the
 //     block's own workgroup, 16 of them took 260 us (4001 x 4160, rank 64).
 #include "stream.hpp"
 
@@ -20,21 +23,34 @@ namespace tg {
 
 namespace {
 
-constexpr int kLoraMore = 15;
+constexpr int kFewRows = 128;
+constexpr int kMore = 32;                 // workgroups for the further adapters of all blocks
+static_assert((kMore & (kMore - 1)) == 0, "a power of two");
+constexpr int kWindow = 512;              // groups of 64 rows that they look through at a time
+constexpr int kStepBytes = 64;            // of K, per row (stream.hpp)
+
+// Rows of a workgroup's block in the form for many rows.
+int many_rows(int64_t M) { return M <= 1024 ? 16 : M <= 2048 ? 32 : 64; }
 
 // The n-th adapter (in the order of its first row) among the rows of `mask`, or
-// -1; same: its rows.  id: one row per lane, -1 without an adapter.
+// -1; same: its rows.  id: one row per lane, -1 without an adapter.  (The result
+// is the same in every lane; saying so keeps the loads behind it from being
+// issued lane value by lane value.)
 __device__ inline int lora_nth(int id, unsigned long long mask, int n, unsigned long long *same)
 {
     unsigned long long left = __ballot(id >= 0) & mask;
+    int e = -1;
     while (left) {
-        const int e = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
-        *same = __ballot(id == e) & mask;
-        if (n-- == 0)
-            return e;
-        left &= ~*same;
+        const int at = __builtin_amdgcn_readlane(id, __builtin_ctzll(left));
+        const unsigned long long rows = __ballot(id == at) & mask;
+        left &= ~rows;
+        if (n-- == 0) {
+            e = at;
+            *same = rows;
+            break;
+        }
     }
-    return -1;
+    return __builtin_amdgcn_readfirstlane(e);
 }
 
 // Adapter e's product with the 16 MB rows from m0 on, ranks 16 NB rb .., K steps
@@ -50,15 +66,16 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, int e, unsigned long
     const auto rX = make_rsrc((const uint8_t *)a.x + (size_t)m0 * kb, (uint32_t)min(a.M - m0, 16 * MB) * kb);
     uint32_t xoff[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-        xoff[i] = keep_or_oob(m0 + i * 16 + r16 < a.M, (uint32_t)(i * 16 + r16) * kb);
+    for (int i = 0; i < MB; ++i)                     // (rows past M have no adapter)
+        xoff[i] = keep_or_oob((same >> (i * 16 + r16)) & 1, (uint32_t)(i * 16 + r16) * kb);
     __amdgpu_buffer_rsrc_t rB[NB];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
         // ranks past the last (of a padded block) read zeros
-        const int r = (rb * NB + j) * 16;
-        rB[j] = make_rsrc((const uint8_t *)a.down + ((size_t)e * a.rank + min(r, a.rank)) * kb,
-                          (uint32_t)max(0, min(a.rank - r, 16)) * kb);
+        const int r = min((rb * NB + j) * 16, a.rank);
+        const uint32_t bytes = (uint32_t)(a.rank - r < 16 ? a.rank - r : 16) * kb;
+        rB[j] = make_rsrc((const uint8_t *)a.down + ((size_t)e * a.rank + r) * kb,
+                          (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
     }
     stream_product<MB, NB, false, false, NB == 1 ? 4 : 2>(rX, xoff, rB, kb, step0, n_steps, red);
     __syncthreads();
@@ -67,15 +84,7 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, int e, unsigned long
         const int row = o / (16 * NB), col = o % (16 * NB), r = rb * 16 * NB + col;
         if (!((same >> row) & 1) || r >= a.rank_pad)
             continue;
-        const float v = s * stream_sum<MB, NB>(red, row, col);
-        if (a.planes) {
-            const size_t at = (size_t)(m0 + row) * a.rank_pad + r;
-            const __bf16 hi = (__bf16)v;
-            ((__bf16 *)a.v)[at] = hi;
-            ((__bf16 *)a.v)[(size_t)a.M * a.rank_pad + at] = (__bf16)(v - (float)hi);
-        } else {
-            ((float *)a.v)[((size_t)part * a.M + m0 + row) * a.rank_pad + r] = v;
-        }
+        a.v[((size_t)part * a.M + m0 + row) * a.rank_pad + r] = s * stream_sum<MB, NB>(red, row, col);
     }
 }
 
@@ -98,35 +107,85 @@ __global__ __launch_bounds__(kStreamThreads, 4) void lora_down_few_kernel(const 
         lora_down<1, 1>(a, m0, e, same, rb, part, red);
 }
 
-// Workgroups 0 .. blocks - 1: the first adapter of each block of 16 MB rows.
-// The rest: kLoraMore per group of 64 rows, for the groups' further adapters.
+// Adapters beyond the first in each of the 4 / MB blocks of 64 rows, together.
+template <int MB>
+__device__ inline int lora_further(int id)
+{
+    int n = 0;
+#pragma unroll
+    for (int b = 0; b < 4 / MB; ++b) {
+        unsigned long long left = __ballot(id >= 0) & ((~0ull >> (64 - 16 * MB)) << (16 * MB * b));
+        for (bool first = true; left; first = false) {
+            left &= ~__ballot(id == __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+            n += !first;
+        }
+    }
+    return __builtin_amdgcn_readfirstlane(n);
+}
+
+// Workgroups more ..: the first adapter of each block of 16 MB rows.  The `more`
+// (0 or kMore) before them: each looks through all rows' adapters for the
+// blocks that have more than one and takes every kMore-th of what it finds.
+// (Before, so that what they find is not left to the end, when every CU is
+// free: 4001 x 4160, rank 64: MORE_MEASURED.)
 template <int MB, int NB>
-__global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const LoraArgs a, int blocks)
+__global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const LoraArgs a, int more)
 {
     __shared__ float red[kStreamWaves][16 * MB][stream_pitch<NB>()];
-    const int l = lane_id(), rb = blockIdx.y;
-    if ((int)blockIdx.x < blocks) {
-        const int m0 = blockIdx.x * 16 * MB;
+    __shared__ int32_t count[kWindow];
+    const int l = lane_id(), rb = blockIdx.y, part = blockIdx.z;
+    if ((int)blockIdx.x >= more) {
+        const int m0 = ((int)blockIdx.x - more) * 16 * MB;
         unsigned long long same = 0;
         const int e = lora_nth(row_id(a, l < 16 * MB && m0 + l < a.M, m0 + l), ~0ull, 0, &same);
         if (e >= 0)
-            lora_down<MB, NB>(a, m0, e, same, rb, 0, red);
+            lora_down<MB, NB>(a, m0, e, same, rb, part, red);
         return;
     }
-    const int more = (int)blockIdx.x - blocks, g = more / kLoraMore, mine = more - g * kLoraMore;
-    const int id = row_id(a, g * 64 + l < a.M, g * 64 + l);
-    int k = 0;
-    for (int b = 0; b < 4 / MB; ++b) {
-        const unsigned long long mask = ((MB == 1 ? 0xFFFFull : 0xFFFFFFFFull)) << (16 * MB * b);
-        for (int n = 1;; ++n) {
-            unsigned long long same = 0;
-            const int e = lora_nth(id, mask, n, &same);
-            if (e < 0)
-                break;
-            if (k++ % kLoraMore != mine)
-                continue;
-            lora_down<MB, NB>(a, g * 64 + 16 * MB * b, e, same >> (16 * MB * b), rb, 0, red);
-            __syncthreads();
+    const int mine = blockIdx.x, groups = (a.M + 63) / 64;
+    int k = 0;                                       // adapters found so far
+    for (int g0 = 0; g0 < groups; g0 += kWindow) {
+        const int here = min(groups - g0, kWindow);
+        __syncthreads();
+        for (int i = wave_id() * 8; i < here; i += kStreamWaves * 8) {
+            int id[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {            // in flight together
+                const int row = (g0 + i + u) * 64 + l;
+                id[u] = row_id(a, row < a.M, row);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int n = lora_further<MB>(id[u]);
+                if (l == 0 && i + u < here)
+                    count[i + u] = n;
+            }
+        }
+        __syncthreads();
+        for (int i = 0; i < here; i += 64) {
+            const int n = i + l < here ? count[i + l] : 0;
+            for (unsigned long long some = __ballot(n > 0); some; some &= some - 1) {
+                const int at = __builtin_ctzll(some), g = g0 + i + at;
+                const int last = k + __builtin_amdgcn_readlane(n, at);
+                if (k + ((mine - k) & (kMore - 1)) >= last) {       // none of these is this workgroup's
+                    k = last;
+                    continue;
+                }
+                const int id = row_id(a, g * 64 + l < a.M, g * 64 + l);
+                for (int b = 0; b < 4 / MB; ++b) {
+                    const unsigned long long mask = (~0ull >> (64 - 16 * MB)) << (16 * MB * b);
+                    for (int nth = 1;; ++nth) {
+                        unsigned long long same = 0;
+                        const int e = lora_nth(id, mask, nth, &same);
+                        if (e < 0)
+                            break;
+                        if ((k++ & (kMore - 1)) != mine)
+                            continue;
+                        lora_down<MB, NB>(a, g * 64 + 16 * MB * b, e, same >> (16 * MB * b), rb, part, red);
+                        __syncthreads();
+                    }
+                }
+            }
         }
     }
 }
@@ -137,9 +196,10 @@ template <int MB, int NB>
 hipError_t many(const LoraArgs &a, int passes, hipStream_t s)
 {
     const int64_t blocks = ((int64_t)a.M + 16 * MB - 1) / (16 * MB);
-    const int64_t more = a.adapters > 1 ? ((int64_t)a.M + 63) / 64 * kLoraMore : 0;
-    hipLaunchKernelGGL((lora_down_many_kernel<MB, NB>), dim3((unsigned)(blocks + more), (unsigned)passes),
-                       dim3(kStreamThreads), 0, s, a, (int)blocks);
+    const int more = a.adapters > 1 ? kMore : 0;
+    hipLaunchKernelGGL((lora_down_many_kernel<MB, NB>),
+                       dim3((unsigned)(blocks + more), (unsigned)passes, (unsigned)a.parts), dim3(kStreamThreads), 0, s,
+                       a, more);
     return hipGetLastError();
 }
 
@@ -153,17 +213,29 @@ hipError_t many_mb(const LoraArgs &a, int blocks, hipStream_t s)
 
 }  // namespace
 
+// Parts of K.  Few rows: 64 KiB of 16 ranks each.  Many: two workgroups per CU
+// with the blocks of rows.  Never less than a step of K per wave.
+int lora_parts(int64_t M, int64_t K)
+{
+    const int64_t rows = many_rows(M), blocks = (M + rows - 1) / rows;
+    const int64_t want = M <= kFewRows ? (K * 2 * 16 + (64 << 10) - 1) / (64 << 10) : 512 / (blocks > 0 ? blocks : 1);
+    const int64_t most = K * 2 / kStepBytes / kStreamWaves;
+    const int64_t p = want < most ? want : most;
+    return (int)(p < 1 ? 1 : p > kLoraParts ? kLoraParts : p);
+}
+
 hipError_t launch_lora_down(const LoraArgs &a, hipStream_t s)
 {
     const int blocks = a.rank_pad / 16;
-    if (a.M <= kLoraFewRows) {
+    if (a.M <= kFewRows) {
         const unsigned rows = (unsigned)((a.M + 15) / 16);
         hipLaunchKernelGGL(lora_down_few_kernel,
                            dim3(rows, (unsigned)(a.adapters < 16 ? a.adapters : 16), (unsigned)(blocks * a.parts)),
                            dim3(kStreamThreads), 0, s, a);
         return hipGetLastError();
     }
-    return a.M <= 8192 ? many_mb<1>(a, blocks, s) : many_mb<2>(a, blocks, s);
+    const int rows = many_rows(a.M);
+    return rows == 16 ? many_mb<1>(a, blocks, s) : rows == 32 ? many_mb<2>(a, blocks, s) : many_mb<4>(a, blocks, s);
 }
 
 }  // namespace tg

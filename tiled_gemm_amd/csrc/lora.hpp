@@ -13,8 +13,8 @@
 // v goes to the matrix unit as two bf16 numbers, v = hi + lo within 2^-17 of it,
 // for twice the MFMAs of a product that is 1 to 3% of the projection's: rounding
 // v to one bf16 would add an error as large as the output's own rounding where
-// the adapters' share of z is large.  The tile kernels read hi and lo; the skinny
-// kernels, whose v is made in parts of K, read fp32 partial sums.
+// the adapters' share of z is large.  v comes as fp32 partial sums over parts of
+// K, which the reader adds.
 #pragma once
 
 #include "device.hpp"
@@ -52,7 +52,8 @@ struct LoraCols {
     }
     __device__ void load(const LoraArgs &lo, int e, u32x4 (&b)[FN]) const
     {
-        const auto ru = make_rsrc((const uint8_t *)lo.up + (size_t)e * bytes, bytes);
+        // (one adapter for the whole wave, which the compiler cannot see)
+        const auto ru = make_rsrc((const uint8_t *)lo.up + (size_t)__builtin_amdgcn_readfirstlane(e) * bytes, bytes);
 #pragma unroll
         for (int j = 0; j < FN; ++j)
             b[j] = buf_load16(ru, off[j], 0);
@@ -68,6 +69,8 @@ __device__ inline void lora_add(f32x4 (*acc)[FN], const u32x4 (&hi)[CH], const u
     const int r16 = lane_id() & 15;
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
+        if (((same >> (i * 16)) & 0xFFFF) == 0)      // none of this block's rows (the same in every lane)
+            continue;
         const bool mine = (same >> (i * 16 + r16)) & 1;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
@@ -87,55 +90,109 @@ __device__ inline int lora_id(const LoraArgs &lo, bool there, int row)
     return (uint32_t)id < (uint32_t)lo.adapters ? id : -1;
 }
 
+// Eight ranks of a row of v from column c on: its parts added, in their order.
+__device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, f32x4 &a, f32x4 &b)
+{
+    const float *const p = (const float *)lo.v + row * lo.rank_pad + c;
+    const size_t part = (size_t)lo.M * lo.rank_pad;
+    f32x4 x[kLoraParts], y[kLoraParts];
+#pragma unroll
+    for (int s = 0; s < kLoraParts; ++s) {
+        const float *const at = p + (s < lo.parts ? s : 0) * part;      // in flight together
+        x[s] = *(const f32x4 *)at;
+        y[s] = *(const f32x4 *)(at + 4);
+    }
+    a = x[0];
+    b = y[0];
+#pragma unroll
+    for (int s = 1; s < kLoraParts; ++s) {
+        if (s < lo.parts) {
+            a += x[s];
+            b += y[s];
+        }
+    }
+}
+
+// LDS of lora_tail: 32 ranks of the tile's rows, hi and lo.
+template <int BM>
+constexpr int lora_lds_bytes() { return BM * 128; }
+
 // acc[i][j] of a tile wave: row block i holds the tile's rows row0 + 16 i .., of
-// which `rows` exist, from row m0 of C on.
-template <int FM, int FN>
-__device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], int m0, int rows, int row0, int col0, int N)
+// which `rows` exist, from row m0 of C on.  All waves of the tile's workgroup
+// call it: v goes through LDS, so that it is read, added up and split once per
+// tile and not once per wave (8192 x 8192 x 2048, rank 32, tiles whose 8 waves
+// share all rows: 12 us less).  LDS may still be read by other waves before the
+// call and after it.
+template <int BM, int THREADS, int FM, int FN>
+__device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8_t *lds, int m0, int rows, int row0,
+                                 int col0, int N)
 {
     constexpr int CH = FM < 4 ? FM : 4;              // row blocks at a time: a row per lane
     constexpr int CHUNKS = FM / CH;
     static_assert(FM % CH == 0, "whole chunks");
     const int l = lane_id(), q = l >> 4, r16 = l & 15;
-    const uint32_t pitch = (uint32_t)lo.rank_pad * 2u;
-    const uint8_t *const hi0 = (const uint8_t *)lo.v + (size_t)m0 * pitch;
-    const auto rh = make_rsrc(hi0, (uint32_t)rows * pitch);
-    const auto rl = make_rsrc(hi0 + (size_t)lo.M * pitch, (uint32_t)rows * pitch);
     int id[CHUNKS];
 #pragma unroll
     for (int c = 0; c < CHUNKS; ++c) {
         const int row = row0 + 16 * CH * c + l;
         id[c] = lora_id(lo, l < 16 * CH && row < rows, m0 + row);
     }
-    const uint32_t off = (uint32_t)(row0 + r16) * pitch + (uint32_t)(8 * q) * 2u;
+    uint8_t *const lds_hi = lds, *const lds_lo = lds + BM * 64;
     for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
         const LoraCols<FN> cols(lo, N, col0, r0);
-        u32x4 b[FN];
+        __syncthreads();
+        for (int it = threadIdx.x; it < BM * 4; it += THREADS) {
+            const int row = it >> 2, c = it & 3;
+            f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
+            if (row < rows)
+                lora_v8(lo, (size_t)(m0 + row), r0 + 8 * c, va, vb);
+            u32x4 hi, low;
+            split_bf16(va, vb, hi, low);
+            *(u32x4 *)(lds_hi + it * 16) = hi;
+            *(u32x4 *)(lds_lo + it * 16) = low;
+        }
+        __syncthreads();
+        u32x4 b[FN], b1[FN];
         int have = -1;                               // the adapter whose columns b holds
         static_for<CHUNKS>([&](auto c_c) {
             constexpr int C = decltype(c_c)::value;
             unsigned long long left = __ballot(id[C] >= 0);
             if (!left)
                 return;
+            int e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
+            if (e != have)
+                cols.load(lo, e, b);
             u32x4 hi[CH], low[CH];
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
-                // rows past the tile's last are past the record count
-                const uint32_t at = off + (uint32_t)(16 * (C * CH + i)) * pitch + (uint32_t)r0 * 2u;
-                hi[i] = buf_load16(rh, at, 0);
-                low[i] = buf_load16(rl, at, 0);
+                const int at = (row0 + 16 * (C * CH + i) + r16) * 64 + q * 16;
+                hi[i] = lds_load16(lds_hi + at);
+                low[i] = lds_load16(lds_lo + at);
             }
-            while (left) {
-                const int e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
+            // One adapter's products from `now` while the next one's columns are
+            // on their way to `next`; false after the last.
+            auto one = [&](const u32x4 (&now)[FN], u32x4 (&next)[FN]) {
                 const unsigned long long same = __ballot(id[C] == e);
+                have = e;
                 left &= ~same;
-                if (e != have) {
-                    cols.load(lo, e, b);
-                    have = e;
+                if (left) {
+                    e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
+                    cols.load(lo, e, next);
                 }
-                lora_add<CH, FN>(&acc[C * CH], hi, low, b, same);
+                lora_add<CH, FN>(&acc[C * CH], hi, low, now, same);
+                return left != 0;
+            };
+            while (one(b, b1)) {
+                if (!one(b1, b)) {
+#pragma unroll
+                    for (int j = 0; j < FN; ++j)
+                        b[j] = b1[j];
+                    break;
+                }
             }
         });
     }
+    __syncthreads();
 }
 
 // The same for a few rows (M <= 64), the adapters shared out to `waves` waves:
@@ -146,8 +203,6 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
 {
     const int l = lane_id(), q = l >> 4, r16 = l & 15;
     const int id = lora_id(lo, l < M, l);
-    const uint32_t pitch = (uint32_t)lo.rank_pad * 4u;
-    const auto rv = make_rsrc(lo.v, (uint32_t)(lo.parts * M) * pitch);
     // The wave's next adapter: its first row's, every waves-th of those left.
     unsigned long long left = 0;
     int n = 0;
@@ -174,15 +229,9 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
         u32x4 hi[MB], low[MB];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
-            const int row = 16 * i + r16;
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
-#pragma unroll
-            for (int s = 0; s < kLoraParts; ++s) {
-                const uint32_t at = keep_or_oob(row < M && s < lo.parts,
-                                                (uint32_t)(s * M + row) * pitch + (uint32_t)(r0 + 8 * q) * 4u);
-                va += __builtin_bit_cast(f32x4, buf_load16(rv, at, 0));
-                vb += __builtin_bit_cast(f32x4, buf_load16(rv, at, 16));
-            }
+            if (16 * i + r16 < M)
+                lora_v8(lo, 16 * i + r16, r0 + 8 * q, va, vb);
             split_bf16(va, vb, hi[i], low[i]);
         }
         while (e >= 0) {
