@@ -15,7 +15,6 @@ struct gemm_group_mlp_plan {
     gemm_group_mlp_plan_info info;
     gemm_group_plan *up, *down;      // the experts' matrices: their checks and their pre-shuffled images
     int act, slots;
-    int up_tiles, down_tiles;
 };
 
 namespace {
@@ -100,8 +99,6 @@ gemm_group_mlp_plan *gemm_group_mlp_plan_create(int groups, int64_t tokens, int 
     static const int kAct[] = {tg::kActNone, tg::kActNone, tg::kActRelu, tg::kActSilu, tg::kActGelu};
     p->act = kAct[epilogue];
     p->slots = (int)slots;
-    p->up_tiles = (int)(N / (gated ? 16 : 32));
-    p->down_tiles = (int)(K / 32);
     gemm_group_mlp_plan_info &I = p->info;
     I.tokens = tokens;
     I.K = K;
@@ -137,7 +134,7 @@ size_t gemm_group_mlp_workspace_bytes(const gemm_group_mlp_plan *plan)
 {
     if (!plan || plan->slots == 0)
         return 0;
-    return h_bytes(plan) + y_bytes(plan) + (size_t)plan->down_tiles * 4;
+    return h_bytes(plan) + y_bytes(plan) + (size_t)plan->info.K / 32 * 4;
 }
 
 int gemm_group_mlp_preshuffle(const gemm_group_mlp_plan *plan, const void *up, void *up_image, const void *down,
@@ -215,8 +212,6 @@ int gemm_group_mlp_run(const gemm_group_mlp_plan *plan, const void *x, const int
     a.slots = plan->slots;
     a.K = (int32_t)I.K;
     a.N = (int32_t)I.N;
-    a.up_tiles = plan->up_tiles;
-    a.down_tiles = plan->down_tiles;
     a.parts = I.groups < plan->slots ? I.groups : plan->slots;
     a.act = plan->act;
     a.gated = I.gated != 0;

@@ -263,10 +263,10 @@ struct MlpArgs {
     void *out;                              // tokens x K bf16
     void *h;                                // workspace: slots x N bf16
     float *y;                               // workspace: slots x K
-    int32_t *done;                          // workspace: one counter per column tile of out
+    int32_t *done;                          // workspace: one counter per 32 columns of out
     int32_t groups, tokens, topk, slots;
     int32_t K, N;                           // the model's width, the experts' hidden width
-    int32_t up_tiles, down_tiles;
+    int32_t up_tiles, down_tiles;           // set by the launcher
     int32_t parts;                          // an upper bound on the active experts
     int32_t act;
     bool gated, e4m3, preshuffled;

@@ -11,10 +11,11 @@
 //     its work by counting bits;
 //   * the launch is two workgroups per CU, which walk the items (active
 //     expert, column tile), so nothing is launched for experts nobody chose;
-//   * an item's 32 weight rows (16 of the gate and the 16 of the linear half
-//     that meet them, or 32 columns of the output) are read straight into
-//     registers in MFMA order, the waves splitting K, each with two sets of
-//     loads in flight; the tokens' rows come from the caches;
+//   * an item's 32 weight rows (16 of the gate and the 16 of the linear half that
+//     meet them, or 32 columns of the output) are read straight into registers
+//     in MFMA order, the waves splitting K, each with two sets of loads in
+//     flight; the tokens' rows come from the caches, once per item (items of 64
+//     weight rows, which halve that, measured 2% faster to 10% slower);
 //   * the second launch's sums over experts meet in the workspace: each item
 //     writes its slots' fp32 sums, and the workgroup that finishes a column tile
 //     last adds the slots of every token in the order of j.  Which workgroup that
@@ -26,16 +27,15 @@ namespace tg {
 namespace {
 
 constexpr int kMlpThreads = kStreamThreads;
-constexpr int kMlpPitch = stream_pitch<2>();
+constexpr int kMlpRows = 32;                       // rows of a pass, at most
 constexpr int kMlpBits = kMaxGroups / 32;          // words of the bitmap of experts
 static_assert(kMlpBits == 32, "one word per lane of half a wave");
 
 // What every workgroup knows of the routing.
 struct MlpShared {
     uint32_t bits[kMlpBits];
-    uint16_t ids[kMlpSlots];         // 0xFFFF: a slot that goes nowhere
-    uint16_t rows[kMlpSlots];        // the current expert's slots, in order
-    int32_t cnt;
+    uint16_t ids[kMlpSlots];                     // 0xFFFF: a slot that goes nowhere
+    uint16_t rows[kStreamWaves][kMlpRows];       // each wave's own copy of the slots of the rows at hand
     int32_t last;
 };
 
@@ -80,53 +80,67 @@ __device__ inline int mlp_expert(const MlpShared &sh, int p)
     return __builtin_amdgcn_readfirstlane(lane * 32 + __builtin_ctz(w));
 }
 
-// The slots of expert e into sh.rows, in order.
-__device__ inline int mlp_rows(MlpShared &sh, int slots, int e)
+// Rows r0 .. r0 + kMlpRows - 1 of expert e (its slots, in order) into this wave's
+// list.  Returns the number of all its rows.  Every wave looks for itself, so
+// nothing has to be waited for.
+__device__ inline int mlp_rows(MlpShared &sh, int slots, int e, int r0)
 {
-    __syncthreads();                                 // the previous expert's rows are no longer read
-    if (wave_id() == 0) {
-        const int l = lane_id();
-        const unsigned long long below = (1ull << l) - 1;
-        int n = 0;
-        for (int s0 = 0; s0 < slots; s0 += 64) {
-            const bool mine = s0 + l < slots && sh.ids[s0 + l] == e;
-            const unsigned long long m = __ballot(mine);
-            if (mine)
-                sh.rows[n + __popcll(m & below)] = (uint16_t)(s0 + l);
-            n += __popcll(m);
-        }
-        if (l == 0)
-            sh.cnt = n;
+    const int l = lane_id();
+    uint16_t *const rows = sh.rows[wave_id()];
+    const unsigned long long below = (1ull << l) - 1;
+    int n = 0;
+    for (int s0 = 0; s0 < slots; s0 += 64) {
+        const bool mine = s0 + l < slots && sh.ids[s0 + l] == e;
+        const unsigned long long m = __ballot(mine);
+        const int at = n + __popcll(m & below) - r0;
+        if (mine && at >= 0 && at < kMlpRows)
+            rows[at] = (uint16_t)(s0 + l);
+        n += __popcll(m);
     }
-    __syncthreads();
-    return __builtin_amdgcn_readfirstlane(sh.cnt);
+    __builtin_amdgcn_wave_barrier();
+    return __builtin_amdgcn_readfirstlane(n);
 }
+
+// LDS of the waves' sums: two sets, so that one barrier per pass is enough (a
+// wave may start on the next pass's products while others still add up this
+// one's).
+template <int MB>
+constexpr int mlp_red() { return kStreamWaves * 16 * MB * stream_pitch<2>(); }
+
+// Steps per set of loads (stream.hpp).  Two sets of two per wave keep 128 KiB in
+// flight on a CU, twice what the latency asks for.  Measured, up / down in us for
+// 2 / 3 / 4: 16 tokens x 4 of 64, 2048 x 1024 bf16 62 / 66 / 71, 37 / 38 / 46 (4
+// spills); the same in e4m3, whose steps hold twice the K, 35 / 52 / 101, 31 / 43 / 96.
+template <int MB>
+constexpr int mlp_u() { return MB == 1 ? 2 : 1; }
 
 }  // namespace
 
-// x -> h.  Column tile c: the gate's and the linear half's columns 16 c .. + 15
-// (GATED), or columns 32 c .. + 31.
-template <int MB, bool E8, bool PRE, int U>
-__device__ inline void mlp_up_item(const MlpArgs &a, const MlpShared &sh, int e, int r0, int cnt, int c, float *lds)
+// x -> h, rows r0 .. of expert e.  Column tile c: the gate's and the linear half's
+// columns 16 c .. + 15 (gated), or columns 32 c .. + 31.
+template <int MB, bool E8, bool PRE>
+__device__ inline void mlp_up_pass(const MlpArgs &a, const MlpShared &sh, int e, int r0, int cnt, int c, float *lds)
 {
-    float(*red)[16 * MB][kMlpPitch] = reinterpret_cast<float(*)[16 * MB][kMlpPitch]>(lds);
+    float(*red)[16 * MB][stream_pitch<2>()] = reinterpret_cast<float(*)[16 * MB][stream_pitch<2>()]>(lds);
+    const uint16_t *const rows = sh.rows[wave_id()];
     const int r16 = lane_id() & 15;
     const uint32_t kb = (uint32_t)a.K * (E8 ? 1u : 2u);
     const int inner = a.gated ? 2 * a.N : a.N;
-    const int n0 = a.gated ? 16 * c : 32 * c, n1 = a.gated ? a.N + 16 * c : 32 * c + 16;
+    const int cols = a.gated ? 16 : 32, n0 = c * cols;
     const uint8_t *const W = (const uint8_t *)a.up + (size_t)e * inner * kb;
+    const int n1 = a.gated ? a.N + n0 : n0 + 16;
     const __amdgpu_buffer_rsrc_t rB[2] = {make_rsrc(W + (size_t)n0 * kb, 16u * kb),
                                           make_rsrc(W + (size_t)n1 * kb, 16u * kb)};
     const auto rX = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.K * 2u);
     uint32_t xoff[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-        const int r = r0 + i * 16 + r16;
-        xoff[i] = keep_or_oob(r < cnt, (uint32_t)(sh.rows[r < cnt ? r : 0] / a.topk) * (uint32_t)a.K * 2u);
+        const int r = i * 16 + r16;
+        const bool there = r0 + r < cnt;
+        xoff[i] = keep_or_oob(there, (uint32_t)(rows[there ? r : 0] / a.topk) * (uint32_t)a.K * 2u);
     }
-    stream_product<MB, 2, E8, PRE, U>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
+    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
     __syncthreads();
-    const int cols = a.gated ? 16 : 32;
     for (int o = threadIdx.x; o < 16 * MB * cols; o += kMlpThreads) {
         const int row = o / cols, col = o - row * cols;
         const int n = n0 + col;
@@ -140,7 +154,7 @@ __device__ inline void mlp_up_item(const MlpArgs &a, const MlpShared &sh, int e,
             z += a.up_bias[at];
         float y = a.act == kActSilu ? epi_silu(z) : epi_act(z, a.act);
         if (a.gated) {
-            float u = stream_sum<MB, 2>(red, row, 16 + col);
+            float u = stream_sum<MB, 2>(red, row, cols + col);
             if (a.up_scale)
                 u *= a.up_scale[at + a.N];
             if (a.up_bias)
@@ -149,7 +163,7 @@ __device__ inline void mlp_up_item(const MlpArgs &a, const MlpShared &sh, int e,
         }
         // h in bf16: the second product's operand, as the layer made of
         // single products keeps it
-        ((__bf16 *)a.h)[(size_t)sh.rows[r0 + row] * a.N + n] = (__bf16)y;
+        ((__bf16 *)a.h)[(size_t)rows[row] * a.N + n] = (__bf16)y;
     }
 }
 
@@ -157,52 +171,55 @@ template <int MB, bool E8, bool PRE>
 __global__ __launch_bounds__(kMlpThreads, 4) void mlp_up_kernel(const MlpArgs a)
 {
     __shared__ MlpShared sh;
-    __shared__ float lds[kStreamWaves * 16 * MB * kMlpPitch];
-    constexpr int U = E8 ? 2 : 4;
+    __shared__ float lds[2][mlp_red<MB>()];
     if (blockIdx.x == 0)
         for (int c = threadIdx.x; c < a.down_tiles; c += kMlpThreads)
             a.done[c] = 0;
     const int active = mlp_mark(sh, a), items = active * a.up_tiles;
-    int p = -1, e = 0, cnt = 0;
+    int set = 0;
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int np = it / a.up_tiles, c = it - np * a.up_tiles;
-        if (np != p) {
-            p = np;
-            e = mlp_expert(sh, p);
-            cnt = mlp_rows(sh, a.slots, e);
-        }
-        for (int r0 = 0; r0 < cnt; r0 += 16 * MB) {
+        const int p = it / a.up_tiles, c = it - p * a.up_tiles;
+        const int e = mlp_expert(sh, p);
+        for (int r0 = 0, cnt = 1; r0 < cnt; r0 += 16 * MB) {
+            cnt = mlp_rows(sh, a.slots, e, r0);
             if (MB == 1 || cnt - r0 <= 16)
-                mlp_up_item<1, E8, PRE, U>(a, sh, e, r0, cnt, c, lds);
+                mlp_up_pass<1, E8, PRE>(a, sh, e, r0, cnt, c, lds[set]);
             else
-                mlp_up_item<MB, E8, PRE, U / 2>(a, sh, e, r0, cnt, c, lds);
-            __syncthreads();                         // the sums have been read
+                mlp_up_pass<MB, E8, PRE>(a, sh, e, r0, cnt, c, lds[set]);
+            set ^= 1;
         }
     }
 }
 
-// h -> the slots' sums, columns 32 c .. + 31 of the output.
-template <int MB, bool E8, bool PRE, int U>
-__device__ inline void mlp_down_item(const MlpArgs &a, const MlpShared &sh, int e, int r0, int cnt, int c, float *lds)
+// h -> the slots' sums, column tile c of the output, in two halves: the
+// waves' products, and behind the barrier their sum.
+template <int MB, bool E8, bool PRE>
+__device__ inline void mlp_down_product(const MlpArgs &a, const MlpShared &sh, int e, int r0, int cnt, int c, float *lds)
 {
-    float(*red)[16 * MB][kMlpPitch] = reinterpret_cast<float(*)[16 * MB][kMlpPitch]>(lds);
+    float(*red)[16 * MB][stream_pitch<2>()] = reinterpret_cast<float(*)[16 * MB][stream_pitch<2>()]>(lds);
+    const uint16_t *const rows = sh.rows[wave_id()];
     const int r16 = lane_id() & 15;
     const uint32_t kb = (uint32_t)a.N * (E8 ? 1u : 2u);
-    const int n0 = 32 * c;
-    const uint8_t *const W = (const uint8_t *)a.down + (size_t)e * a.K * kb;
-    const __amdgpu_buffer_rsrc_t rB[2] = {make_rsrc(W + (size_t)n0 * kb, 16u * kb),
-                                          make_rsrc(W + (size_t)(n0 + 16) * kb, 16u * kb)};
+    const uint8_t *const W = (const uint8_t *)a.down + ((size_t)e * a.K + 32 * c) * kb;
+    const __amdgpu_buffer_rsrc_t rB[2] = {make_rsrc(W, 16u * kb), make_rsrc(W + (size_t)16 * kb, 16u * kb)};
     const auto rX = make_rsrc(a.h, (uint32_t)a.slots * (uint32_t)a.N * 2u);
     uint32_t xoff[MB];
 #pragma unroll
     for (int i = 0; i < MB; ++i) {
-        const int r = r0 + i * 16 + r16;
-        xoff[i] = keep_or_oob(r < cnt, (uint32_t)sh.rows[r < cnt ? r : 0] * (uint32_t)a.N * 2u);
+        const int r = i * 16 + r16;
+        const bool there = r0 + r < cnt;
+        xoff[i] = keep_or_oob(there, (uint32_t)rows[there ? r : 0] * (uint32_t)a.N * 2u);
     }
-    stream_product<MB, 2, E8, PRE, U>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
-    __syncthreads();
+    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
+}
+
+template <int MB>
+__device__ inline void mlp_down_sum(const MlpArgs &a, const MlpShared &sh, int e, int r0, int cnt, int c, const float *lds)
+{
+    const float(*red)[16 * MB][stream_pitch<2>()] = reinterpret_cast<const float(*)[16 * MB][stream_pitch<2>()]>(lds);
+    const uint16_t *const rows = sh.rows[wave_id()];
     for (int o = threadIdx.x; o < 16 * MB * 32; o += kMlpThreads) {
-        const int row = o / 32, n = n0 + o % 32;
+        const int row = o / 32, n = 32 * c + o % 32;
         if (r0 + row >= cnt)
             continue;
         const size_t at = (size_t)e * a.K + n;
@@ -211,64 +228,89 @@ __device__ inline void mlp_down_item(const MlpArgs &a, const MlpShared &sh, int 
             z *= a.down_scale[at];
         if (a.down_bias)
             z += a.down_bias[at];
-        __hip_atomic_store(a.y + (size_t)sh.rows[r0 + row] * a.K + n, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        __hip_atomic_store(a.y + (size_t)rows[row] * a.K + n, z, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
 }
 
+// Column tile c of the output, from its slots' sums.
+__device__ inline void mlp_combine(const MlpArgs &a, const MlpShared &sh, int c)
+{
+    for (int o = threadIdx.x; o < a.tokens * 32; o += kMlpThreads) {
+        const int t = o / 32, n = 32 * c + o % 32;
+        float sum = 0.f;
+#pragma unroll 4
+        for (int j = 0; j < a.topk; ++j) {
+            const int s = t * a.topk + j;
+            if (sh.ids[s] == 0xFFFF)
+                continue;                            // nor is its weight read as a factor
+            const float y = __hip_atomic_load(a.y + (size_t)s * a.K + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            sum = fmaf(a.weights ? a.weights[s] : 1.f, y, sum);
+        }
+        const size_t at = (size_t)t * a.K + n;
+        if (a.residual)
+            sum += (float)((const __bf16 *)a.residual)[at];
+        ((__bf16 *)a.out)[at] = (__bf16)sum;
+    }
+}
+
+// An item's sums have to be out before it counts as done, and the workgroup
+// that counts a column tile's last item adds them up.  The XCDs' L2 caches are
+// not coherent with each other, so the sums are written through and read past
+// them (agent scope on each access), and waiting for the stores is all a
+// release has to do.  With a release fence instead, which writes the whole L2
+// back for every wave, the launch took 88 us for one token and 652 us for 16.
+//
+// Neither the stores nor the counter's reply are waited for where they are
+// issued: a pass first runs the products of the next item, and what went out in
+// the pass before has long arrived by then.  `stored`: the column tile whose last
+// sums the previous pass stored; `counted`: the one whose counter it raised, the
+// reply in `reply` (thread 0).
 template <int MB, bool E8, bool PRE>
 __global__ __launch_bounds__(kMlpThreads, 4) void mlp_down_kernel(const MlpArgs a)
 {
     __shared__ MlpShared sh;
-    __shared__ float lds[kStreamWaves * 16 * MB * kMlpPitch];
-    constexpr int U = E8 ? 2 : 4;
+    __shared__ float lds[2][mlp_red<MB>()];
     // Without any active expert the column tiles still have to be written.
     const int active = mlp_mark(sh, a), parts = max(active, 1), items = parts * a.down_tiles;
-    int p = -1, e = 0, cnt = 0;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int np = it / a.down_tiles, c = it - np * a.down_tiles;
-        if (active && np != p) {
-            p = np;
-            e = mlp_expert(sh, p);
-            cnt = mlp_rows(sh, a.slots, e);
-        }
-        for (int r0 = 0; r0 < cnt; r0 += 16 * MB) {
-            if (MB == 1 || cnt - r0 <= 16)
-                mlp_down_item<1, E8, PRE, U>(a, sh, e, r0, cnt, c, lds);
-            else
-                mlp_down_item<MB, E8, PRE, U / 2>(a, sh, e, r0, cnt, c, lds);
-            __syncthreads();
-        }
-        // This item's sums are out before it counts as done; the last one of
-        // the column tile sees all of them.  The XCDs' L2 caches are not
-        // coherent with each other, so the sums are written through and read
-        // past them (agent scope on each access), and waiting for the stores
-        // is all a release has to do.  With a release fence instead, which
-        // writes the whole L2 back for every wave, the launch took 88 us for one
-        // token and 652 us for 16.
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (threadIdx.x == 0)
-            sh.last = __hip_atomic_fetch_add(&a.done[c], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == parts - 1;
-        __syncthreads();
-        if (!sh.last)
-            continue;
-        asm volatile("" ::: "memory");
-        for (int o = threadIdx.x; o < a.tokens * 32; o += kMlpThreads) {
-            const int t = o / 32, n = 32 * c + o % 32;
-            float sum = 0.f;
-#pragma unroll 4
-            for (int j = 0; j < a.topk; ++j) {
-                const int s = t * a.topk + j;
-                if (sh.ids[s] == 0xFFFF)
-                    continue;                        // nor is its weight read as a factor
-                const float y = __hip_atomic_load(a.y + (size_t)s * a.K + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                sum = fmaf(a.weights ? a.weights[s] : 1.f, y, sum);
+    int it = blockIdx.x, r0 = 0, set = 0, stored = -1, counted = -1, reply = 0;
+    while (it < items || stored >= 0 || counted >= 0) {
+        int p = 0, c = -1, e = 0, cnt = 0;
+        if (it < items) {
+            p = it / a.down_tiles;
+            c = it - p * a.down_tiles;
+            if (active) {
+                e = mlp_expert(sh, p);
+                cnt = mlp_rows(sh, a.slots, e, r0);
+                if (MB == 1 || cnt - r0 <= 16)
+                    mlp_down_product<1, E8, PRE>(a, sh, e, r0, cnt, c, lds[set]);
+                else
+                    mlp_down_product<MB, E8, PRE>(a, sh, e, r0, cnt, c, lds[set]);
             }
-            const size_t at = (size_t)t * a.K + n;
-            if (a.residual)
-                sum += (float)((const __bf16 *)a.residual)[at];
-            ((__bf16 *)a.out)[at] = (__bf16)sum;
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the previous pass's sums are out
+        if (threadIdx.x == 0)
+            sh.last = counted >= 0 && reply == parts - 1;
+        __syncthreads();
+        const int ready = sh.last ? counted : -1;
+        counted = stored;
+        if (threadIdx.x == 0 && stored >= 0)
+            reply = __hip_atomic_fetch_add(&a.done[stored], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        stored = -1;
+        if (c >= 0) {
+            if (MB == 1 || cnt - r0 <= 16)
+                mlp_down_sum<1>(a, sh, e, r0, cnt, c, lds[set]);
+            else
+                mlp_down_sum<MB>(a, sh, e, r0, cnt, c, lds[set]);
+            set ^= 1;
+            r0 += 16 * MB;
+            if (r0 >= cnt) {                                   // the item's last rows
+                stored = c;
+                it += gridDim.x;
+                r0 = 0;
+            }
+        }
+        if (ready >= 0)
+            mlp_combine(a, sh, ready);
     }
 }
 
@@ -289,7 +331,7 @@ hipError_t launch(const MlpArgs &a, hipStream_t s)
 }
 
 template <int MB>
-hipError_t launch_mb(const MlpArgs &a, hipStream_t s)
+hipError_t launch_tokens(const MlpArgs &a, hipStream_t s)
 {
     if (a.e4m3)
         return a.preshuffled ? launch<MB, true, true>(a, s) : launch<MB, true, false>(a, s);
@@ -298,11 +340,14 @@ hipError_t launch_mb(const MlpArgs &a, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_mlp(const MlpArgs &a, hipStream_t s)
+hipError_t launch_mlp(const MlpArgs &args, hipStream_t s)
 {
+    MlpArgs a = args;
+    a.up_tiles = a.N / (a.gated ? 16 : 32);
+    a.down_tiles = a.K / 32;
     // Up to 16 tokens an expert has one block of rows (unless a token names it
     // more than once, which the loop over its rows takes care of).
-    return a.tokens <= 16 ? launch_mb<1>(a, s) : launch_mb<2>(a, s);
+    return a.tokens <= 16 ? launch_tokens<1>(a, s) : launch_tokens<2>(a, s);
 }
 
 }  // namespace tg

@@ -87,12 +87,15 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
     };
     Set s0, s1;
     load(0, s0);
-    for (int t = 0; t < nt; t += 2 * U) {
-        load(t + U, s1);
+    load(U, s1);
+    for (int t = 2 * U; t < nt; t += 2 * U) {
         compute(s0);
-        load(t + 2 * U, s0);
+        load(t, s0);
         compute(s1);
+        load(t + U, s1);
     }
+    compute(s0);
+    compute(s1);
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
