@@ -211,11 +211,15 @@ def test_grad(kind, M, N, groups, dtype):
         r = slice(off[g], off[g + 1])
         bound = (2.0 ** -19 + (off[g + 1] - off[g]) * 2.0 ** -24) * mag[r].sum(0)
         assert np.all(np.abs(db[g].double().cpu().numpy() - full[r].sum(0)) <= bound)
-    # the same gradient as from the decoded values kept in fp32, bit for bit, and in place over d_c
+    # the gradient from the decoded values: the same bits (GELU: another evaluation within the same tolerance)
     Z = torch.from_numpy(z).float().to(dtype).cuda()       # exact (4 significant bits)
     ref = torch.full_like(D, 4.0)
     tg.gemm_act_grad(M, N, CODE[dtype], tg.EPILOGUES[kind], D.data_ptr(), Z.data_ptr(), ref.data_ptr(), **args)
-    assert torch.equal(ref, out)
+    if kind == "bias_gelu":
+        assert np.all(np.abs((ref - out).double().cpu().numpy()) <= 2 * (tol + HALF[dtype] * np.abs(want)))
+    else:
+        assert torch.equal(ref, out)
+    # in place over d_c
     tg.gemm_act_grad_ckpt(M, N, CODE[dtype], tg.EPILOGUES[kind], D.data_ptr(), q.data_ptr(), s.data_ptr(), D.data_ptr(),
                           **args)
     m = torch.from_numpy(inside).cuda()[:, None]

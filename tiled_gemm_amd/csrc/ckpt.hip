@@ -11,7 +11,7 @@
 //
 // Both kernels are bound by HBM: pack reads 2 (bf16) or 4 bytes and writes
 // 33 / 32 per element, unpack the other way round.  A wave takes 512 columns of
-// kCkptRows rows, a lane 8 consecutive columns of each (16-byte loads), so 4
+// kPackRows rows, a lane 8 consecutive columns of each (16-byte loads), so 4
 // lanes hold a block and find its largest magnitude with two lane moves.
 #include "cols.hpp"
 
@@ -22,10 +22,19 @@ namespace {
 constexpr int kCkptThreads = 256;
 constexpr int kCkptWaves = kCkptThreads / 64;
 constexpr int kCkptCols = 512;
-// Rows per wave: their loads are in flight together.
-constexpr int kCkptRows = 4;
+// Rows per wave: their loads are in flight together.  Measured, 1 / 2 / 4 / 8 rows in
+// us: pack 8192 x 8192 bf16 39.1 / 36.9 / 40.3 / 42.7; unpack 8192 x 4096 with SiLU
+// 2 / 3 / 4 / 8: 22.5 / 21.9 / 21.4 / 22.6.
+constexpr int kPackRows = 2, kUnpackRows = 4;
 // A launch has fewer than 2^32 threads.
 constexpr int64_t kCkptBlocks = (int64_t)1 << 23;
+
+template <int ACT>
+__device__ inline float ckpt_act(float z)
+{
+    float e;
+    return ACT == kActSilu ? epi_silu(z) : ACT == kActGelu ? z * normal_cdf(z, e) : epi_act(z, ACT);
+}
 
 // The largest of the 4 lanes' values that share a block.
 __device__ inline uint32_t quad_max(uint32_t x)
@@ -34,15 +43,15 @@ __device__ inline uint32_t quad_max(uint32_t x)
     return max(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
 }
 
-// A wave's place: 512 columns from col, rows row .. row + kCkptRows - 1.
+// A wave's place: 512 columns of ROWS rows; `col` is this lane's first column.
 struct CkptPlace {
-    int64_t row;
-    int64_t col;      // this lane's first column
+    int64_t row, col;
 };
+template <int ROWS>
 __device__ inline CkptPlace ckpt_place(uint32_t unit, uint32_t chunks)
 {
     const uint32_t r = unit / chunks;
-    return CkptPlace{(int64_t)r * kCkptRows, (int64_t)(unit - r * chunks) * kCkptCols + lane_id() * 8};
+    return CkptPlace{(int64_t)r * ROWS, (int64_t)(unit - r * chunks) * kCkptCols + lane_id() * 8};
 }
 
 }  // namespace
@@ -52,11 +61,11 @@ __global__ __launch_bounds__(kCkptThreads) void ckpt_pack_kernel(const CkptArgs 
 {
     const uint32_t step = gridDim.x * kCkptWaves;
     for (uint32_t u = __builtin_amdgcn_readfirstlane(blockIdx.x * kCkptWaves + wave_id()); u < a.units; u += step) {
-        const CkptPlace p = ckpt_place(u, a.chunks);
+        const CkptPlace p = ckpt_place<kPackRows>(u, a.chunks);
         const bool in = p.col < a.N;
-        float v[kCkptRows][8];
+        float v[kPackRows][8];
 #pragma unroll
-        for (int r = 0; r < kCkptRows; ++r) {
+        for (int r = 0; r < kPackRows; ++r) {
             if (in && p.row + r < a.M) {
                 load8<T>(a.src, (size_t)(p.row + r) * a.N + p.col, v[r]);
             } else {
@@ -66,30 +75,33 @@ __global__ __launch_bounds__(kCkptThreads) void ckpt_pack_kernel(const CkptArgs 
             }
         }
 #pragma unroll
-        for (int r = 0; r < kCkptRows; ++r) {
-            // Magnitudes compare as their bits; what is not finite does not count.
+        for (int r = 0; r < kPackRows; ++r) {
+            // Magnitudes compare as their bits.
             uint32_t top = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t m = __builtin_bit_cast(uint32_t, v[r][i]) & 0x7FFFFFFFu;
-                top = max(top, m < 0x7F800000u ? m : 0u);
+            for (int i = 0; i < 8; ++i)
+                top = max(top, __builtin_bit_cast(uint32_t, v[r][i]) & 0x7FFFFFFFu);
+            if (__ballot(top >= 0x7F800000u)) {
+                // e4m3 has no infinity: it is stored as NaN, like NaN itself,
+                // and neither counts for the block's scale
+                top = 0;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t m = __builtin_bit_cast(uint32_t, v[r][i]) & 0x7FFFFFFFu;
+                    top = max(top, m < 0x7F800000u ? m : 0u);
+                    v[r][i] = m < 0x7F800000u ? v[r][i] : as_f32(0x7FC00000u);
+                }
             }
             top = quad_max(top);
             // top = 1.f 2^(e - 127); 448 = 1.75 2^8
             const int byte = max((int)(top >> 23) - 8 + ((top & 0x7FFFFFu) > 0x600000u ? 1 : 0), 0);
             const float inv = as_f32((uint32_t)(254 - byte) << 23);
-            uint32_t w[2] = {0, 0};
+            uint32_t w[2];
 #pragma unroll
-            for (int i = 0; i < 8; i += 4) {
-                float x[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    // e4m3 has no infinity: it is stored as NaN, like NaN itself
-                    const uint32_t m = __builtin_bit_cast(uint32_t, v[r][i + j]) & 0x7FFFFFFFu;
-                    x[j] = m < 0x7F800000u ? v[r][i + j] * inv : as_f32(0x7FC00000u);
-                }
-                int t = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
-                w[i / 4] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], t, true);
+            for (int h = 0; h < 2; ++h) {
+                const float *x = v[r] + 4 * h;
+                const int t = __builtin_amdgcn_cvt_pk_fp8_f32(x[0] * inv, x[1] * inv, 0, false);
+                w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2] * inv, x[3] * inv, t, true);
             }
             if (in && p.row + r < a.M) {
                 *(u32x2 *)(a.q + (size_t)(p.row + r) * a.N + p.col) = u32x2{w[0], w[1]};
@@ -105,20 +117,26 @@ __global__ __launch_bounds__(kCkptThreads) void ckpt_unpack_kernel(const CkptArg
 {
     const uint32_t step = gridDim.x * kCkptWaves;
     for (uint32_t u = __builtin_amdgcn_readfirstlane(blockIdx.x * kCkptWaves + wave_id()); u < a.units; u += step) {
-        const CkptPlace p = ckpt_place(u, a.chunks);
+        const CkptPlace p = ckpt_place<kUnpackRows>(u, a.chunks);
         if (p.col >= a.N)
             continue;
+        u32x2 w[kUnpackRows];
+        uint32_t byte[kUnpackRows];
 #pragma unroll
-        for (int r = 0; r < kCkptRows; ++r) {
-            if (p.row + r >= a.M)
-                break;
-            const size_t at = (size_t)(p.row + r) * a.N + p.col;
+        for (int r = 0; r < kUnpackRows; ++r) {        // (past the last row: that row again)
+            const int64_t row = min(p.row + r, a.M - 1);
+            w[r] = *(const u32x2 *)(a.q + (size_t)row * a.N + p.col);
+            byte[r] = a.scales[(size_t)row * a.blocks + p.col / kCkptBlock];
+        }
+#pragma unroll
+        for (int r = 0; r < kUnpackRows; ++r) {
             float v[8];
-            ckpt_load8(a.q, at, e8m0_value(a.scales[(size_t)(p.row + r) * a.blocks + p.col / kCkptBlock]), v);
+            ckpt_value8(w[r], e8m0_value(byte[r]), v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = ACT == kActSilu ? epi_silu(v[i]) : epi_act(v[i], ACT);
-            store8<T>(a.out, at, v);
+                v[i] = ckpt_act<ACT>(v[i]);
+            if (p.row + r < a.M)
+                store8<T>(a.out, (size_t)(p.row + r) * a.N + p.col, v);
         }
     }
 }
@@ -147,16 +165,19 @@ void unpack(const CkptArgs &a, hipStream_t s)
 
 }  // namespace
 
-int64_t ckpt_units(int64_t M, int64_t N)
-{
-    return (M + kCkptRows - 1) / kCkptRows * ((N + kCkptCols - 1) / kCkptCols);
-}
+namespace {
+
+int64_t units(int64_t M, int64_t N, int rows) { return (M + rows - 1) / rows * ((N + kCkptCols - 1) / kCkptCols); }
+
+}  // namespace
+
+int64_t ckpt_units(int64_t M, int64_t N) { return units(M, N, kPackRows < kUnpackRows ? kPackRows : kUnpackRows); }
 
 hipError_t launch_ckpt_pack(const CkptArgs &args, hipStream_t s)
 {
     CkptArgs a = args;
     a.chunks = (uint32_t)((a.N + kCkptCols - 1) / kCkptCols);
-    a.units = (uint32_t)ckpt_units(a.M, a.N);
+    a.units = (uint32_t)units(a.M, a.N, kPackRows);
     if (a.type == kOutF32)
         hipLaunchKernelGGL(ckpt_pack_kernel<kOutF32>, ckpt_grid(a), dim3(kCkptThreads), 0, s, a);
     else
@@ -168,7 +189,7 @@ hipError_t launch_ckpt_unpack(const CkptArgs &args, hipStream_t s)
 {
     CkptArgs a = args;
     a.chunks = (uint32_t)((a.N + kCkptCols - 1) / kCkptCols);
-    a.units = (uint32_t)ckpt_units(a.M, a.N);
+    a.units = (uint32_t)units(a.M, a.N, kUnpackRows);
     if (a.type == kOutF32)
         unpack<kOutF32>(a, s);
     else

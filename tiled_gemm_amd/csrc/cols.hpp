@@ -26,6 +26,14 @@ __device__ inline void load8(const void *base, size_t at, float (&v)[8])
     }
 }
 
+// Two fp32 -> two bf16 (nearest even) in one instruction, packed low-first.
+__device__ inline uint32_t pack_pair(float lo, float hi)
+{
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
+}
+
 template <int T>
 __device__ inline void store8(void *base, size_t at, const float (&v)[8])
 {
@@ -33,8 +41,8 @@ __device__ inline void store8(void *base, size_t at, const float (&v)[8])
         *(f32x4 *)((float *)base + at) = f32x4{v[0], v[1], v[2], v[3]};
         *(f32x4 *)((float *)base + at + 4) = f32x4{v[4], v[5], v[6], v[7]};
     } else {
-        *(u32x4 *)((uint16_t *)base + at) = u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+        *(u32x4 *)((uint16_t *)base + at) = u32x4{pack_pair(v[0], v[1]), pack_pair(v[2], v[3]),
+                                                  pack_pair(v[4], v[5]), pack_pair(v[6], v[7])};
     }
 }
 
@@ -46,17 +54,17 @@ constexpr int kCkptBlock = 32;
 
 typedef float f32x2_t __attribute__((ext_vector_type(2)));
 
+// 2^(byte - 127): the exponent in place, except that 0 is 2^-127, a fraction bit,
+// which also makes a NaN of 255.
 __device__ inline float e8m0_value(uint32_t byte)
 {
-    return byte == 255u ? __builtin_nanf("") : (byte == 0u ? as_f32(0x00400000u) : as_f32(byte << 23));
+    return as_f32(byte << 23 | (((byte + 1) & 0xFF) < 2 ? 0x00400000u : 0u));
 }
 
-// Eight elements (8-byte aligned) times their block's scale.  The product of
-// a 4-bit significand and a power of two is exact in fp32 unless it leaves
-// fp32's range.
-__device__ inline void ckpt_load8(const uint8_t *q, size_t at, float step, float (&v)[8])
+// Eight elements times their block's scale.  The product of a 4-bit significand
+// and a power of two is exact in fp32 unless it leaves fp32's range.
+__device__ inline void ckpt_value8(u32x2 w, float step, float (&v)[8])
 {
-    const u32x2 w = *(const u32x2 *)(q + at);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const f32x2_t lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[h], false);
@@ -66,6 +74,23 @@ __device__ inline void ckpt_load8(const uint8_t *q, size_t at, float step, float
         v[4 * h + 2] = hi.x * step;
         v[4 * h + 3] = hi.y * step;
     }
+}
+
+// Phi(z) and e = exp(-z^2 / 2), for GELU beside the checkpoint's few bytes, where
+// erff (two branches of long polynomials) bounded the kernels: Abramowitz and
+// Stegun, 7.1.26, erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 + p x), within
+// 1.5e-7 for x = |z| / sqrt 2 >= 0, so Phi is within 2^-23 and has no cancellation
+// where it is small.  NaN passes through.
+__device__ inline float normal_cdf(float z, float &e)
+{
+    e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170368f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752440f, 1.f));
+    float y = fmaf(t, 1.061405429f, -1.453152027f);
+    y = fmaf(t, y, 1.421413741f);
+    y = fmaf(t, y, -0.284496736f);
+    y = fmaf(t, y, 0.254829592f);
+    y = 0.5f * t * y * e;
+    return z < 0.f ? y : 1.f - y;
 }
 
 }  // namespace tg

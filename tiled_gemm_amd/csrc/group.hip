@@ -313,7 +313,9 @@ hipError_t launch_group_combine_grad(const CombineArgs &args, hipStream_t s)
 
 // ---------------------------------------------------------------------------
 // d_z = d_c * act'(z) and its column sums per row group, z as saved or from its
-// 8-bit checkpoint (CK).  Bound: HBM (6 bytes per element in bf16, 5.03 with CK).  Rows are cut into chunks that never cross a group; a
+// 8-bit checkpoint (CK).  Bound: HBM (6 bytes per element in bf16, 5.03 with CK;
+// 8192 x 8192 with d_bias 73 to 77 us, 4.6 TB/s; neither the order of the
+// workgroups nor 1, 2 or 4 rows at a time changes it).  Rows are cut into chunks that never cross a group; a
 // workgroup takes one chunk and 512 columns, lane l of each of its 4 waves
 // columns 8 l .. 8 l + 7, wave w the chunk's rows w, w + 4, ...  The chunk's
 // column sums go to the workspace and a second, small launch adds a group's
@@ -348,6 +350,34 @@ __device__ inline float act_slope(float z)
     return 1.f;
 }
 
+// The same slopes with fewer instructions, for the checkpoint's fewer bytes.
+// SiLU: the logistic factor takes any z, NaN among them, so only the other factor
+// is kept finite, in one instruction; equal to act_slope bit for bit while
+// |z| <= 100.  GELU: normal_cdf for erff (1013 x 2112 in 16 groups: 10.4 -> 8.0 us).
+__device__ inline float silu_slope(float z)
+{
+    const float p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
+    return p * (1.f + __builtin_amdgcn_fmed3f(z, -100.f, 100.f) * (1.f - p));
+}
+
+__device__ inline float gelu_slope(float z)
+{
+    float e;
+    const float cdf = normal_cdf(z, e);
+    return cdf + __builtin_amdgcn_fmed3f(z, -100.f, 100.f) * (0.39894228040143267794f * e);
+}
+
+template <int ACT, bool CK>
+__device__ inline float grad_slope(float z)
+{
+    if constexpr (CK && ACT == kActSilu)
+        return silu_slope(z);
+    else if constexpr (CK && ACT == kActGelu)
+        return gelu_slope(z);
+    else
+        return act_slope<ACT>(z);
+}
+
 }  // namespace
 
 template <int T, int ACT, bool CK>
@@ -378,13 +408,13 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs
             if constexpr (ACT != kActNone) {
                 float z[8];
                 if constexpr (CK)
-                    ckpt_load8((const uint8_t *)a.z, at,
-                               e8m0_value(a.scales[(size_t)(r0 + r) * a.blocks + col / kCkptBlock]), z);
+                    ckpt_value8(*(const u32x2 *)((const uint8_t *)a.z + at),
+                                e8m0_value(a.scales[(size_t)(r0 + r) * a.blocks + col / kCkptBlock]), z);
                 else
                     load8<T>(a.z, at, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    d[i] *= act_slope<ACT>(z[i]);
+                    d[i] *= grad_slope<ACT, CK>(z[i]);
             }
             store8<T>(a.d_z, at, d);
 #pragma unroll
