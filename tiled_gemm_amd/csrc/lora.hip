@@ -53,11 +53,13 @@ __device__ inline int lora_nth(int id, unsigned long long mask, int n, unsigned 
     return __builtin_amdgcn_readfirstlane(e);
 }
 
-// Adapter e's product with the 16 MB rows from m0 on, ranks 16 NB rb .., K steps
-// of part `part`; stored for the rows of `same` (bit r: row m0 + r).
-template <int MB, int NB>
-__device__ inline void lora_down(const LoraArgs &a, int m0, int e, unsigned long long same, int rb, int part,
-                                 float (*red)[16 * MB][stream_pitch<NB>()])
+// The product of the 16 MB rows from m0 on (those of `there`, bit r: row m0 + r)
+// with an adapter, ranks 16 NB rb .., K steps of part `part`.  find(same) names the
+// adapter (-1: none, nothing is stored) and the rows that are stored; it is called
+// behind the first loads of x.
+template <int MB, int NB, typename FindAdapter>
+__device__ inline void lora_down(const LoraArgs &a, int m0, unsigned long long there, FindAdapter find_adapter, int rb,
+                                 int part, float (*red)[16 * MB][stream_pitch<NB>()])
 {
     const int r16 = lane_id() & 15;
     const uint32_t kb = (uint32_t)a.K * 2u;
@@ -66,20 +68,24 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, int e, unsigned long
     const auto rX = make_rsrc((const uint8_t *)a.x + (size_t)m0 * kb, (uint32_t)min(a.M - m0, 16 * MB) * kb);
     uint32_t xoff[MB];
 #pragma unroll
-    for (int i = 0; i < MB; ++i)                     // (rows past M have no adapter)
-        xoff[i] = keep_or_oob((same >> (i * 16 + r16)) & 1, (uint32_t)(i * 16 + r16) * kb);
-    __amdgpu_buffer_rsrc_t rB[NB];
+    for (int i = 0; i < MB; ++i)                     // (rows past M are past the record count)
+        xoff[i] = keep_or_oob((there >> (i * 16 + r16)) & 1, (uint32_t)(i * 16 + r16) * kb);
+    unsigned long long same = 0;
+    float s = 1.f;
+    auto find = [&](__amdgpu_buffer_rsrc_t (&rB)[NB]) {
+        const int e = find_adapter(&same), any = e < 0 ? 0 : e;
+        s = a.scale ? a.scale[any] : 1.f;
 #pragma unroll
-    for (int j = 0; j < NB; ++j) {
-        // ranks past the last (of a padded block) read zeros
-        const int r = min((rb * NB + j) * 16, a.rank);
-        const uint32_t bytes = (uint32_t)(a.rank - r < 16 ? a.rank - r : 16) * kb;
-        rB[j] = make_rsrc((const uint8_t *)a.down + ((size_t)e * a.rank + r) * kb,
-                          (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
-    }
-    stream_product<MB, NB, false, false, NB == 1 ? 4 : 2>(rX, xoff, rB, kb, step0, n_steps, red);
+        for (int j = 0; j < NB; ++j) {
+            // ranks past the last (of a padded block) read zeros
+            const int r = min((rb * NB + j) * 16, a.rank);
+            const uint32_t bytes = e < 0 ? 0u : (uint32_t)(a.rank - r < 16 ? a.rank - r : 16) * kb;
+            rB[j] = make_rsrc((const uint8_t *)a.down + ((size_t)any * a.rank + r) * kb,
+                              (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
+        }
+    };
+    stream_product<MB, NB, false, false, NB == 1 ? 4 : 2>(rX, xoff, find, kb, step0, n_steps, red);
     __syncthreads();
-    const float s = a.scale ? a.scale[e] : 1.f;
     for (int o = threadIdx.x; o < 16 * MB * 16 * NB; o += kStreamThreads) {
         const int row = o / (16 * NB), col = o % (16 * NB), r = rb * 16 * NB + col;
         if (!((same >> row) & 1) || r >= a.rank_pad)
@@ -103,8 +109,13 @@ __global__ __launch_bounds__(kStreamThreads, 4) void lora_down_few_kernel(const 
     const int rb = blockIdx.z / a.parts, part = blockIdx.z - rb * a.parts;
     unsigned long long same = 0;
     const int e = lora_nth(row_id(a, l < 16 && m0 + l < a.M, m0 + l), ~0ull, blockIdx.y, &same);
-    if (e >= 0)
-        lora_down<1, 1>(a, m0, e, same, rb, part, red);
+    if (e < 0)                                       // (most workgroups, where rows share adapters)
+        return;
+    auto find = [&](unsigned long long *rows) {
+        *rows = same;
+        return e;
+    };
+    lora_down<1, 1>(a, m0, same, find, rb, part, red);
 }
 
 // Adapters beyond the first in each of the 4 / MB blocks of 64 rows, together.
@@ -136,10 +147,9 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
     const int l = lane_id(), rb = blockIdx.y, part = blockIdx.z;
     if ((int)blockIdx.x >= more) {
         const int m0 = ((int)blockIdx.x - more) * 16 * MB;
-        unsigned long long same = 0;
-        const int e = lora_nth(row_id(a, l < 16 * MB && m0 + l < a.M, m0 + l), ~0ull, 0, &same);
-        if (e >= 0)
-            lora_down<MB, NB>(a, m0, e, same, rb, part, red);
+        const int id = row_id(a, l < 16 * MB && m0 + l < a.M, m0 + l);
+        auto find = [&](unsigned long long *rows) { return lora_nth(id, ~0ull, 0, rows); };
+        lora_down<MB, NB>(a, m0, ~0ull, find, rb, part, red);
         return;
     }
     const int mine = blockIdx.x, groups = (a.M + 63) / 64;
@@ -181,7 +191,11 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
                             break;
                         if ((k++ & (kMore - 1)) != mine)
                             continue;
-                        lora_down<MB, NB>(a, g * 64 + 16 * MB * b, e, same >> (16 * MB * b), rb, part, red);
+                        auto find = [&](unsigned long long *rows) {
+                            *rows = same >> (16 * MB * b);
+                            return e;
+                        };
+                        lora_down<MB, NB>(a, g * 64 + 16 * MB * b, same >> (16 * MB * b), find, rb, part, red);
                         __syncthreads();
                     }
                 }

@@ -152,16 +152,25 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
             *(u32x4 *)(lds_lo + it * 16) = low;
         }
         __syncthreads();
-        u32x4 b[FN], b1[FN];
-        int have = -1;                               // the adapter whose columns b holds
+        u32x4 b[3][FN];
+        int have = -1;                               // the adapter whose columns b[0] holds
         static_for<CHUNKS>([&](auto c_c) {
             constexpr int C = decltype(c_c)::value;
             unsigned long long left = __ballot(id[C] >= 0);
             if (!left)
                 return;
-            int e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
-            if (e != have)
-                cols.load(lo, e, b);
+            auto pop = [&]() {                       // the next adapter among the chunk's rows, or -1
+                if (!left)
+                    return -1;
+                const int e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
+                left &= ~__ballot(id[C] == e);
+                return e;
+            };
+            int e0 = pop(), e1 = pop();
+            if (e0 != have)
+                cols.load(lo, e0, b[0]);
+            if (e1 >= 0)
+                cols.load(lo, e1, b[1]);
             u32x4 hi[CH], low[CH];
 #pragma unroll
             for (int i = 0; i < CH; ++i) {
@@ -169,24 +178,23 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
                 hi[i] = lds_load16(lds_hi + at);
                 low[i] = lds_load16(lds_lo + at);
             }
-            // One adapter's products from `now` while the next one's columns are
-            // on their way to `next`; false after the last.
-            auto one = [&](const u32x4 (&now)[FN], u32x4 (&next)[FN]) {
-                const unsigned long long same = __ballot(id[C] == e);
-                have = e;
-                left &= ~same;
-                if (left) {
-                    e = __builtin_amdgcn_readlane(id[C], __builtin_ctzll(left));
-                    cols.load(lo, e, next);
-                }
+            // One adapter's products from `now` while the columns of the one after
+            // the next start on their way to `ahead` (a decode row's adapter has
+            // not been read before: its columns come from HBM); false after the last.
+            auto one = [&](const u32x4 (&now)[FN], u32x4 (&ahead)[FN]) {
+                const unsigned long long same = __ballot(id[C] == e0);
+                have = e0;
+                e0 = e1;
+                e1 = pop();
+                if (e1 >= 0)
+                    cols.load(lo, e1, ahead);
                 lora_add<CH, FN>(&acc[C * CH], hi, low, now, same);
-                return left != 0;
+                return e0 >= 0;
             };
-            while (one(b, b1)) {
-                if (!one(b1, b)) {
-#pragma unroll
-                    for (int j = 0; j < FN; ++j)
-                        b[j] = b1[j];
+            while (one(b[0], b[2])) {
+                have = -1;
+                if (!one(b[1], b[0]) || !one(b[2], b[1])) {
+                    have = -1;
                     break;
                 }
             }

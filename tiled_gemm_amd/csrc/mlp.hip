@@ -129,8 +129,10 @@ __device__ inline void mlp_up_pass(const MlpArgs &a, const MlpShared &sh, int e,
     const int cols = a.gated ? 16 : 32, n0 = c * cols;
     const uint8_t *const W = (const uint8_t *)a.up + (size_t)e * inner * kb;
     const int n1 = a.gated ? a.N + n0 : n0 + 16;
-    const __amdgpu_buffer_rsrc_t rB[2] = {make_rsrc(W + (size_t)n0 * kb, 16u * kb),
-                                          make_rsrc(W + (size_t)n1 * kb, 16u * kb)};
+    auto find = [&](__amdgpu_buffer_rsrc_t (&rB)[2]) {
+        rB[0] = make_rsrc(W + (size_t)n0 * kb, 16u * kb);
+        rB[1] = make_rsrc(W + (size_t)n1 * kb, 16u * kb);
+    };
     const auto rX = make_rsrc(a.x, (uint32_t)a.tokens * (uint32_t)a.K * 2u);
     uint32_t xoff[MB];
 #pragma unroll
@@ -139,7 +141,7 @@ __device__ inline void mlp_up_pass(const MlpArgs &a, const MlpShared &sh, int e,
         const bool there = r0 + r < cnt;
         xoff[i] = keep_or_oob(there, (uint32_t)(rows[there ? r : 0] / a.topk) * (uint32_t)a.K * 2u);
     }
-    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
+    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
     __syncthreads();
     for (int o = threadIdx.x; o < 16 * MB * cols; o += kMlpThreads) {
         const int row = o / cols, col = o - row * cols;
@@ -201,7 +203,10 @@ __device__ inline void mlp_down_product(const MlpArgs &a, const MlpShared &sh, i
     const int r16 = lane_id() & 15;
     const uint32_t kb = (uint32_t)a.N * (E8 ? 1u : 2u);
     const uint8_t *const W = (const uint8_t *)a.down + ((size_t)e * a.K + 32 * c) * kb;
-    const __amdgpu_buffer_rsrc_t rB[2] = {make_rsrc(W, 16u * kb), make_rsrc(W + (size_t)16 * kb, 16u * kb)};
+    auto find = [&](__amdgpu_buffer_rsrc_t (&rB)[2]) {
+        rB[0] = make_rsrc(W, 16u * kb);
+        rB[1] = make_rsrc(W + (size_t)16 * kb, 16u * kb);
+    };
     const auto rX = make_rsrc(a.h, (uint32_t)a.slots * (uint32_t)a.N * 2u);
     uint32_t xoff[MB];
 #pragma unroll
@@ -210,7 +215,7 @@ __device__ inline void mlp_down_product(const MlpArgs &a, const MlpShared &sh, i
         const bool there = r0 + r < cnt;
         xoff[i] = keep_or_oob(there, (uint32_t)rows[there ? r : 0] * (uint32_t)a.N * 2u);
     }
-    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, rB, kb, 0, (int)(kb / 64), red);
+    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
 }
 
 template <int MB>

@@ -34,11 +34,12 @@ __device__ inline u32x4 fp8x8_to_bf16(uint32_t lo, uint32_t hi)
 //   rB[j]   weight block j: 16 rows of kb bytes (or their image)
 // Lane 16 q + r holds bytes 16 q .. of row r of a step, one MFMA of bf16 or two
 // of e4m3 (E8: elements 16 q .. + 7 and + 8 .. + 15).  Two sets of U steps are in
-// flight per wave.
-template <int MB, int NB, bool E8, bool PRE, int U>
-__device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t (&xoff)[MB],
-                                      const __amdgpu_buffer_rsrc_t (&rB)[NB], uint32_t kb, int step0, int steps,
-                                      float (*red)[16 * MB][stream_pitch<NB>()])
+// flight per wave.  find(rB) names the weight blocks; it is called once the first
+// loads of x are on their way, so that what it waits for (which adapter the rows
+// have, say) is waited for beside them.
+template <int MB, int NB, bool E8, bool PRE, int U, typename Find>
+__device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t (&xoff)[MB], Find find, uint32_t kb,
+                                      int step0, int steps, float (*red)[16 * MB][stream_pitch<NB>()])
 {
     constexpr int H = E8 ? 2 : 1;                    // MFMAs (and 16-byte loads of a row of x) per step
     const int w = wave_id(), l = lane_id(), q = l >> 4, r16 = l & 15;
@@ -49,7 +50,8 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
         u32x4 b[U][NB];
         u32x4 x[U][MB][H];
     };
-    auto load = [&](int t0, Set &s) {
+    __amdgpu_buffer_rsrc_t rB[NB];
+    auto load_b = [&](int t0, Set &s) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const bool in = t0 + u < nt;
@@ -57,6 +59,13 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
 #pragma unroll
             for (int j = 0; j < NB; ++j)
                 s.b[u][j] = buf_load16(rB[j], keep_or_oob(in, boff), k * (PRE ? 1024u : 64u));
+        }
+    };
+    auto load_x = [&](int t0, Set &s) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = t0 + u < nt;
+            const uint32_t k = in ? (uint32_t)(first + t0 + u) : 0u;
 #pragma unroll
             for (int i = 0; i < MB; ++i)
 #pragma unroll
@@ -64,6 +73,10 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
                     s.x[u][i][h] = buf_load16(rX, keep_or_oob(in, xoff[i] + (uint32_t)(q * 16 * H + 16 * h)),
                                               k * (64u * H));
         }
+    };
+    auto load = [&](int t0, Set &s) {
+        load_b(t0, s);
+        load_x(t0, s);
         issue_fence();
     };
     f32x4 acc[MB][NB];
@@ -86,7 +99,10 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
                 }
     };
     Set s0, s1;
-    load(0, s0);
+    load_x(0, s0);
+    issue_fence();
+    find(rB);
+    load_b(0, s0);
     load(U, s1);
     for (int t = 2 * U; t < nt; t += 2 * U) {
         compute(s0);
