@@ -108,11 +108,12 @@ template <int MB>
 constexpr int mlp_red() { return kStreamWaves * 16 * MB * stream_pitch<2>(); }
 
 // Steps per set of loads (stream.hpp).  Two sets of two per wave keep 128 KiB in
-// flight on a CU, twice what the latency asks for.  Measured, up / down in us for
-// 2 / 3 / 4: 16 tokens x 4 of 64, 2048 x 1024 bf16 62 / 66 / 71, 37 / 38 / 46 (4
-// spills); the same in e4m3, whose steps hold twice the K, 35 / 52 / 101, 31 / 43 / 96.
-template <int MB>
-constexpr int mlp_u() { return MB == 1 ? 2 : 1; }
+// flight on a CU, twice what the latency asks for.  Measured, us for 1 / 2 / 3 / 4, 16
+// tokens x 4 of 64, 2048 x 1024: up 64 / 61 / 66 / 71, down 38 / 37 / 38 / 46 in bf16;
+// up 36 / 35 / 52 / 101, down 27 / 32 / 43 / 96 in e4m3 (whose steps hold twice the K,
+// and whose second product leaves a wave only two or so).
+template <int MB, bool E8, bool DOWN>
+constexpr int mlp_u() { return MB == 1 && !(E8 && DOWN) ? 2 : 1; }
 
 }  // namespace
 
@@ -141,7 +142,7 @@ __device__ inline void mlp_up_pass(const MlpArgs &a, const MlpShared &sh, int e,
         const bool there = r0 + r < cnt;
         xoff[i] = keep_or_oob(there, (uint32_t)(rows[there ? r : 0] / a.topk) * (uint32_t)a.K * 2u);
     }
-    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
+    stream_product<MB, 2, E8, PRE, mlp_u<MB, E8, false>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
     __syncthreads();
     for (int o = threadIdx.x; o < 16 * MB * cols; o += kMlpThreads) {
         const int row = o / cols, col = o - row * cols;
@@ -215,7 +216,7 @@ __device__ inline void mlp_down_product(const MlpArgs &a, const MlpShared &sh, i
         const bool there = r0 + r < cnt;
         xoff[i] = keep_or_oob(there, (uint32_t)rows[there ? r : 0] * (uint32_t)a.N * 2u);
     }
-    stream_product<MB, 2, E8, PRE, mlp_u<MB>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
+    stream_product<MB, 2, E8, PRE, mlp_u<MB, E8, true>()>(rX, xoff, find, kb, 0, (int)(kb / 64), red);
 }
 
 template <int MB>

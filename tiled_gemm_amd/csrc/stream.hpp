@@ -43,8 +43,7 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
 {
     constexpr int H = E8 ? 2 : 1;                    // MFMAs (and 16-byte loads of a row of x) per step
     const int w = wave_id(), l = lane_id(), q = l >> 4, r16 = l & 15;
-    const int per = (steps + kStreamWaves - 1) / kStreamWaves;
-    const int first = step0 + w * per, nt = max(0, min(per, step0 + steps - first));
+    const int first = step0 + w * steps / kStreamWaves, nt = step0 + (w + 1) * steps / kStreamWaves - first;
     const uint32_t boff = PRE ? (uint32_t)l * 16u : (uint32_t)r16 * kb + (uint32_t)q * 16u;
     struct Set {
         u32x4 b[U][NB];
