@@ -52,13 +52,13 @@ __device__ inline void stream_product(__amdgpu_buffer_rsrc_t rX, const uint32_t 
     __amdgpu_buffer_rsrc_t rB[NB];
     auto load_b = [&](int t0, Set &s) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const bool in = t0 + u < nt;
-            const uint32_t k = in ? (uint32_t)(first + t0 + u) : 0u;
+        for (int j = 0; j < NB; ++j)                 // (steps inside: the halves of a line one after the other)
 #pragma unroll
-            for (int j = 0; j < NB; ++j)
+            for (int u = 0; u < U; ++u) {
+                const bool in = t0 + u < nt;
+                const uint32_t k = in ? (uint32_t)(first + t0 + u) : 0u;
                 s.b[u][j] = buf_load16(rB[j], keep_or_oob(in, boff), k * (PRE ? 1024u : 64u));
-        }
+            }
     };
     auto load_x = [&](int t0, Set &s) {
 #pragma unroll
