@@ -959,9 +959,13 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
     return GEMM_OK;
 }
 
+// Room for v, whatever the number of adapters.
 size_t lora_v_bytes(const gemm_plan *plan, int rank)
 {
-    const size_t n = (size_t)tg::lora_parts(plan->info.M, plan->info.K) * (size_t)plan->info.M * (size_t)((rank + 31) / 32 * 32) * 4;
+    const int64_t M = plan->info.M, K = plan->info.K;
+    const int pad = (rank + 31) / 32 * 32;
+    const int one = tg::lora_parts(M, K, pad, 1), many = tg::lora_parts(M, K, pad, 2);
+    const size_t n = (size_t)(one > many ? one : many) * (size_t)M * (size_t)pad * 4;
     return (n + 255) / 256 * 256;
 }
 
@@ -1136,7 +1140,7 @@ int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, 
     l.rank_pad = (lora->rank + 31) / 32 * 32;
     l.M = (int32_t)I.M;
     l.K = (int32_t)I.K;
-    l.parts = tg::lora_parts(I.M, I.K);
+    l.parts = tg::lora_parts(I.M, I.K, l.rank_pad, l.adapters);
     const hipError_t r = tg::launch_lora_down(l, stream);
     if (r != hipSuccess)
         return fail(GEMM_ERR_HIP, "adapters' launch: %s", hipGetErrorString(r));

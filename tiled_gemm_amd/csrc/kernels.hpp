@@ -50,10 +50,10 @@ struct LoraArgs {
     int32_t adapters, rank;
     int32_t rank_pad;           // rank rounded up to 32 (the rest of v is zeros)
     int32_t M, K;
-    int32_t parts;              // partial sums over K, lora_parts(M, K)
+    int32_t parts;              // partial sums over K, lora_parts()
 };
 constexpr int kLoraParts = 4;
-int lora_parts(int64_t M, int64_t K);
+int lora_parts(int64_t M, int64_t K, int rank_pad, int adapters);
 hipError_t launch_lora_down(const LoraArgs &, hipStream_t);
 
 struct TiledArgs {

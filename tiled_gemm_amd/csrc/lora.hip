@@ -9,13 +9,15 @@
 // to kLoraParts), which the reader adds.  Two forms, by the number of rows:
 //   * up to kFewRows (decode): the adapters' matrices are the bytes, most rows
 //     have one of their own.  A workgroup takes one adapter of 16 rows, 16 of its
-//     ranks and one part.
+//     ranks and one part.  (200 rows, K 4160, rank 64: 11.5 us in packed prompts,
+//     18.7 with 16 adapters in random order; the other form 10.8 and 29.6.  600
+//     rows: 21.0 packed against 12.4.)
 //   * above (prompts, training): x is the bytes, and blocks of rows mostly have
 //     one adapter.  A workgroup takes the first adapter of 16, 32 or 64 rows (so
 //     many that the parts still give every CU one) with up to 64 ranks at once,
 //     x read once for them.  The further adapters of a block (decode rows in
-//     front of the prompts, a prompt's end) are shared out to kMore workgroups
-//     more, which read the rows of theirs only.  One after the other in the
+//     front of the prompts, a prompt's end) are shared out to some workgroups
+//     more (more_of), which read the rows of theirs only.  One after the other in the
 //     block's own workgroup, 16 of them took 260 us (4001 x 4160, rank 64).
 #include "stream.hpp"
 
@@ -23,11 +25,15 @@ namespace tg {
 
 namespace {
 
-constexpr int kFewRows = 128;
-constexpr int kMore = 32;                 // workgroups for the further adapters of all blocks
-static_assert((kMore & (kMore - 1)) == 0, "a power of two");
+constexpr int kFewRows = 256;
+// Workgroups for the further adapters of all blocks: many beside small blocks, few
+// beside those of 64 rows, which fill the CUs with one round of workgroups (see
+// lora_down_many_kernel).
+constexpr int more_of(int rows) { return rows == 64 ? 16 : 64; }
 constexpr int kWindow = 512;              // groups of 64 rows that they look through at a time
 constexpr int kStepBytes = 64;            // of K, per row (stream.hpp)
+
+int more_wgs(int adapters, int rows) { return adapters > 1 ? more_of(rows) : 0; }
 
 // Rows of a workgroup's block in the form for many rows.
 int many_rows(int64_t M) { return M <= 1024 ? 16 : M <= 2048 ? 32 : 64; }
@@ -140,14 +146,18 @@ __device__ inline int lora_further(int id)
 // Workgroups more ..: the first adapter of each block of 16 MB rows.  The `more`
 // (0 or kMore) before them: each looks through all rows' adapters for the
 // blocks that have more than one and takes every kMore-th of what it finds.
-// (Before, so that what they find is not left to the end.  4001 x 4160, rank 64:
-// 29.5 us with 16 decode rows and 6 prompts of up to 16 adapters, 15.3 with one
-// adapter.)
+// (Before, so that what they find is not left to the end.)  4001 x 4160, rank 64,
+// 16 decode rows and 6 prompts of up to 16 adapters: 18.5 us with 16 of them (and
+// three parts), 30 with 32, a second round of workgroups, 27 with 8; with one
+// adapter 14.8.  Blocks of 16 rows: 64 take 12.4 us for 600 packed rows and 113
+// for 1000 rows with 16 adapters in random order, 16 take 11.3 and 216.
 template <int MB, int NB>
 __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const LoraArgs a, int more)
 {
     __shared__ float red[kStreamWaves][16 * MB][stream_pitch<NB>()];
     __shared__ int32_t count[kWindow];
+    constexpr int kMore = more_of(16 * MB);
+    static_assert((kMore & (kMore - 1)) == 0, "a power of two");
     const int l = lane_id(), rb = blockIdx.y, part = blockIdx.z;
     if ((int)blockIdx.x >= more) {
         const int m0 = ((int)blockIdx.x - more) * 16 * MB;
@@ -188,12 +198,14 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
                 const int id = row_id(a, g * 64 + l < a.M, g * 64 + l);
                 for (int b = 0; b < 4 / MB; ++b) {
                     const unsigned long long mask = (~0ull >> (64 - 16 * MB)) << (16 * MB * b);
-                    for (int nth = 1;; ++nth) {
-                        unsigned long long same = 0;
-                        const int e = lora_nth(id, mask, nth, &same);
-                        if (e < 0)
-                            break;
-                        if ((k++ & (kMore - 1)) != mine)
+                    unsigned long long left = __ballot(id >= 0) & mask;
+                    for (bool first = true; left; first = false) {
+                        // (the same in every lane, see lora_nth)
+                        const int e = __builtin_amdgcn_readfirstlane(
+                            __builtin_amdgcn_readlane(id, __builtin_ctzll(left)));
+                        const unsigned long long same = __ballot(id == e) & mask;
+                        left &= ~same;
+                        if (first || (k++ & (kMore - 1)) != mine)
                             continue;
                         auto find = [&](unsigned long long *rows) {
                             *rows = same >> (16 * MB * b);
@@ -214,7 +226,7 @@ template <int MB, int NB>
 hipError_t many(const LoraArgs &a, int passes, hipStream_t s)
 {
     const int64_t blocks = ((int64_t)a.M + 16 * MB - 1) / (16 * MB);
-    const int more = a.adapters > 1 ? kMore : 0;
+    const int more = more_wgs(a.adapters, 16 * MB);
     hipLaunchKernelGGL((lora_down_many_kernel<MB, NB>),
                        dim3((unsigned)(blocks + more), (unsigned)passes, (unsigned)a.parts), dim3(kStreamThreads), 0, s,
                        a, more);
@@ -231,15 +243,32 @@ hipError_t many_mb(const LoraArgs &a, int blocks, hipStream_t s)
 
 }  // namespace
 
-// Parts of K.  Few rows: 64 KiB of 16 ranks each.  Many: two workgroups per CU
-// with the blocks of rows.  Never less than a step of K per wave.
-int lora_parts(int64_t M, int64_t K)
+// Parts of K, never less than a step of K per wave.  Few rows: 64 KiB of 16 ranks
+// each.  Many: as many as bring the launch's rounds of workgroups nearest to full
+// (fewest rounds over parts; the LDS of 64 rows by 64 ranks leaves one workgroup
+// per CU, that of the others two or more).  4001 x 4160 and rank 64 in packed
+// prompts: 22.3 us with the 3 parts that make one round of them, 24.6 with 4;
+// 8000 x 4160 with one adapter 28.3 with 2, 31.0 with 4.
+int lora_parts(int64_t M, int64_t K, int rank_pad, int adapters)
 {
-    const int64_t rows = many_rows(M), blocks = (M + rows - 1) / rows;
-    const int64_t want = M <= kFewRows ? (K * 2 * 16 + (64 << 10) - 1) / (64 << 10) : 512 / (blocks > 0 ? blocks : 1);
     const int64_t most = K * 2 / kStepBytes / kStreamWaves;
-    const int64_t p = want < most ? want : most;
-    return (int)(p < 1 ? 1 : p > kLoraParts ? kLoraParts : p);
+    const int64_t cap = most < 1 ? 1 : most > kLoraParts ? kLoraParts : most;
+    if (M <= kFewRows) {
+        const int64_t p = (K * 2 * 16 + (64 << 10) - 1) / (64 << 10);
+        return (int)(p < 1 ? 1 : p > cap ? cap : p);
+    }
+    const int64_t rows = many_rows(M), passes = rank_pad == 32 ? 1 : (rank_pad + 63) / 64;
+    const int64_t wgs = ((M + rows - 1) / rows + more_wgs(adapters, (int)rows)) * passes;
+    const int64_t slots = rows == 64 && rank_pad > 32 ? 256 : 512;
+    int64_t best = 1, best_rounds = 0;
+    for (int64_t p = 1; p <= cap; ++p) {
+        const int64_t rounds = (wgs * p + slots - 1) / slots;
+        if (p == 1 || rounds * best < best_rounds * p) {
+            best = p;
+            best_rounds = rounds;
+        }
+    }
+    return (int)best;
 }
 
 hipError_t launch_lora_down(const LoraArgs &a, hipStream_t s)
