@@ -36,7 +36,7 @@ struct MlpShared {
     uint32_t bits[kMlpBits];
     uint16_t ids[kMlpSlots];                     // 0xFFFF: a slot that goes nowhere
     uint16_t rows[kStreamWaves][kMlpRows];       // each wave's own copy of the slots of the rows at hand
-    int32_t last;
+    int32_t last[2];                             // of the passes in turn: read behind a barrier, written before the next
 };
 
 // Marks the experts that some slot names.  Returns their number.
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(kMlpThreads, 4) void mlp_down_kernel(const MlpArgs 
     __shared__ float lds[2][mlp_red<MB>()];
     // Without any active expert the column tiles still have to be written.
     const int active = mlp_mark(sh, a), parts = max(active, 1), items = parts * a.down_tiles;
-    int it = blockIdx.x, r0 = 0, set = 0, stored = -1, counted = -1, reply = 0;
+    int it = blockIdx.x, r0 = 0, set = 0, stored = -1, counted = -1, reply = 0, turn = 0;
     while (it < items || stored >= 0 || counted >= 0) {
         int p = 0, c = -1, e = 0, cnt = 0;
         if (it < items) {
@@ -295,9 +295,10 @@ __global__ __launch_bounds__(kMlpThreads, 4) void mlp_down_kernel(const MlpArgs 
         }
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // the previous pass's sums are out
         if (threadIdx.x == 0)
-            sh.last = counted >= 0 && reply == parts - 1;
+            sh.last[turn] = counted >= 0 && reply == parts - 1;
         __syncthreads();
-        const int ready = sh.last ? counted : -1;
+        const int ready = sh.last[turn] ? counted : -1;
+        turn ^= 1;
         counted = stored;
         if (threadIdx.x == 0 && stored >= 0)
             reply = __hip_atomic_fetch_add(&a.done[stored], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
