@@ -770,7 +770,8 @@ int gemm_act_grad(int64_t M, int64_t N, int type, int epilogue, const void *d_c,
  *   q       M x N bytes row-major, 16-byte aligned;
  *   scales  M x ceil(N / 32) bytes row-major, E8M0: s = 2^(byte - 127), 255 NaN.
  * 33 / 32 bytes per element instead of 2 or 4, each within 2^-4 of itself (and
- * within 2^-10 s near zero).  With N a multiple of 64 the pair is an operand of
+ * within 2^-10 s near zero); a finite |x| of 2^128 (1 - 2^-5) or more is rounded
+ * to 2^128, which fp32 and bf16 hold as infinity.  With N a multiple of 64 the pair is an operand of
  * the MXFP8 products (q as A or B, scales through gemm_preshuffle_bscale).
  *
  * The usual use: gemm_run_res or gemm_group_run saves the pre-activation z,
