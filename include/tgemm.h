@@ -357,7 +357,8 @@ int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, voi
  *   residual, preact  as for gemm_run_res;
  *   workspace  gemm_lora_workspace_bytes(plan, rank) bytes, 16-byte aligned,
  *            contents undefined before and after (v, and the partial tiles
- *            where the plan splits K).  Calls that share one must not overlap
+ *            where K is split: above 8192 where the plan splits, and where its
+ *            options say so).  Calls that share one must not overlap
  *            in time.
  * Asynchronous; allocates nothing; two launches (three with split K).  GEMM_OK
  * or an error.

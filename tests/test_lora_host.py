@@ -68,8 +68,13 @@ def test_workspace():
         assert [p.lora_workspace_bytes(r) for r in (0, 4, 20, 264, -16)] == [0] * 5
     with tg.Plan(7, 64, 8192, BF, BT) as p:                    # decode: K in 4 parts of 16 ranks x 4 KiB
         assert p.lora_workspace_bytes(16) == pad(4 * 7 * 32 * 4)
-    with tg.Plan(256, 4096, 8192, BF, PRE) as p:               # partial tiles behind v
+    with tg.Plan(256, 4096, 16384, BF, PRE) as p:              # partial tiles behind v
         assert p.workspace_bytes() > 0
+        assert p.lora_workspace_bytes(32) == pad(4 * 256 * 32 * 4) + p.workspace_bytes()
+    with tg.Plan(256, 4096, 8192, BF, PRE) as p:               # adapters split K above 8192 only
+        assert p.workspace_bytes() > 0
+        assert p.lora_workspace_bytes(32) == pad(4 * 256 * 32 * 4)
+    with tg.Plan(256, 4096, 8192, BF, PRE, splits=3) as p:     # or where the caller says so
         assert p.lora_workspace_bytes(32) == pad(4 * 256 * 32 * 4) + p.workspace_bytes()
     with tg.Plan(0, 64, 128, BF, BT) as p:
         assert p.lora_workspace_bytes(16) == 0

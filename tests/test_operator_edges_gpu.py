@@ -141,6 +141,15 @@ def test_first_half_forms(M, adapters, rank, mix):
     c.check()
 
 
+def test_adapters_with_the_planners_split():
+    """K above 8192 is split where the plan splits: partial tiles behind v."""
+    c = LoraCase(200, 528, 9216, 40, 4, kind="bias_silu", residual=True, preact=True)
+    assert c.need > 4 * 200 * 64 * 4 + 255
+    c.run()
+    torch.cuda.synchronize()
+    c.check()
+
+
 @pytest.mark.parametrize("dtype", [BF16, torch.float32])
 @pytest.mark.parametrize("kind", ["bias_relu", "bias_silu", "bias_gelu"])
 def test_grad_behind_every_code(kind, dtype):

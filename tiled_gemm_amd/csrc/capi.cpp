@@ -28,6 +28,7 @@ struct gemm_plan {
     // when splitting does not pay.
     const tg::TiledVariant *split_v;
     int32_t splits, split_steps, split_grid, split_tiles_m, split_tiles_n, split_group_m;
+    bool split_forced;                 // the caller's number of slices
     // The kernel behind gemm_run_res (kernel == 0): `tiled`, or smaller tiles
     // where those would leave CUs idle.  nullptr: no extended epilogue.
     const tg::TiledVariant *ex_v;
@@ -308,6 +309,7 @@ void plan_split(gemm_plan *p, int kc, int forced)
         return;
     p->split_v = v;
     p->splits = s;
+    p->split_forced = forced > 0;
     p->split_steps = per;
     p->split_tiles_m = (int32_t)tm;
     p->split_tiles_n = (int32_t)tn;
@@ -959,6 +961,17 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
     return GEMM_OK;
 }
 
+// Whether adapters go with split K.  Up to K = 8192 the tiles with more steps in
+// flight (plan_ex) take less than slices, partial tiles and their sum: 4 adapters
+// of rank 32, split against not: 310 x 1264 x 2432 51 / 24 us, 200 x 4096 x 4096
+// 48 / 31, 900 x 2048 x 8192 80 / 73, 512 x 8192 x 8192 95 / 100; above it splitting
+// does: 300 x 2048 x 12288 68 / 79, 128 x 2048 x 16384 60 / 89.  Plans without such
+// tiles split as they are: 700 x 8192 x 8192 120 / 176.
+bool lora_splits(const gemm_plan *plan)
+{
+    return plan->splits > 1 && (plan->split_forced || plan->ex_v == plan->tiled || plan->kbytes > 8192 * 2);
+}
+
 // Room for v, whatever the number of adapters.
 size_t lora_v_bytes(const gemm_plan *plan, int rank)
 {
@@ -1061,7 +1074,7 @@ size_t gemm_lora_workspace_bytes(const gemm_plan *plan, int rank)
 {
     if (!plan || plan->info.M == 0 || plan->info.N == 0 || rank < 8 || rank > GEMM_LORA_MAX_RANK || rank % 8 != 0)
         return 0;
-    return lora_v_bytes(plan, rank) + workspace_bytes(plan);
+    return lora_v_bytes(plan, rank) + (lora_splits(plan) ? workspace_bytes(plan) : 0);
 }
 
 int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, const gemm_epilogue_args *epi,
@@ -1095,7 +1108,7 @@ int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, 
         return fail(GEMM_ERR_UNSUPPORTED, "M above 2^24");
     if (I.M == 0 || I.N == 0)
         return ok(), GEMM_OK;
-    const bool split = plan->splits > 1;
+    const bool split = lora_splits(plan);
     if (split ? !plan->split_v->launch_lora_part
               : I.kernel == 1 ? !plan->skinny->launch_lora : !plan->ex_v || !plan->ex_v->launch_lora)
         return fail(GEMM_ERR_UNSUPPORTED, "this kernel choice has no adapters (GEMM_KERNEL_AUTO, "
