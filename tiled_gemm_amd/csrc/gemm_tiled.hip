@@ -70,7 +70,10 @@ struct TiledCfg {
 
 template <int BM, int BN, int WGM, int WGN, int ELEM, bool BPRE, int OUT, bool BKN, bool EX, bool GRP = false, int NS = 2,
           bool LORA = false>
-__global__ __launch_bounds__(kTiledThreads, 1) void gemm_tiled_kernel(const TiledArgs p0)
+// (Adapters' columns take more registers than a second workgroup per CU leaves,
+// which the two-stage tiles live on: bounded, 2500 x 2048 x 4096 with rank 64 takes
+// 75 us instead of 128, without adapters 61.)
+__global__ __launch_bounds__(kTiledThreads, LORA && NS == 2 ? 2 : 1) void gemm_tiled_kernel(const TiledArgs p0)
 {
     TiledArgs p = p0;
     using Cfg = TiledCfg<BM, BN, WGM, WGN, ELEM, BPRE, OUT, BKN, NS>;
