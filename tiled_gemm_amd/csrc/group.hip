@@ -314,9 +314,9 @@ hipError_t launch_group_combine_grad(const CombineArgs &args, hipStream_t s)
 // ---------------------------------------------------------------------------
 // d_z = d_c * act'(z) and its column sums per row group, z as saved or from its
 // 8-bit checkpoint (CK).  Bound: HBM (6 bytes per element in bf16, 5.03 with CK;
-// 8192 x 8192 with d_bias 73 to 77 us, 4.6 TB/s; neither the order of the
-// workgroups nor 1, 2 or 4 rows at a time changes it).  Rows are cut into chunks that never cross a group; a
-// workgroup takes one chunk and 512 columns, lane l of each of its 4 waves
+// 8192 x 8192 from its checkpoint with d_bias 73 to 79 us, 4.3 to 4.6 TB/s; neither
+// the order of the workgroups nor 1, 2 or 4 rows at a time changes it).  Rows are
+// cut into chunks that never cross a group; a workgroup takes one chunk and 512 columns, lane l of each of its 4 waves
 // columns 8 l .. 8 l + 7, wave w the chunk's rows w, w + 4, ...  The chunk's
 // column sums go to the workspace and a second, small launch adds a group's
 // chunks in order: no atomics, so d_bias is the same on every run.

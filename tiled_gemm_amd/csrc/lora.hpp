@@ -120,8 +120,13 @@ constexpr int lora_lds_bytes() { return BM * 128; }
 // acc[i][j] of a tile wave: row block i holds the tile's rows row0 + 16 i .., of
 // which `rows` exist, from row m0 of C on.  All waves of the tile's workgroup
 // call it: v goes through LDS, so that it is read, added up and split once per
-// tile and not once per wave (4001 x 4096 x 4160, rank 64: 8 us less in all).  LDS may still be read by other waves before the
-// call and after it.
+// tile and not once per wave (with the parts of K that are added up here:
+// 8192 x 8192 x 2048, rank 32, 337 -> 328 us).  LDS may still be read by other waves
+// before the call and after it.  What it costs: about 3 us per tile (that shape:
+// 13 us of 328 in four rounds of tiles), and some 250 cycles for each adapter
+// beyond the first among a wave's 64 rows, a chain of ballots and two dependent
+// MFMAs; their columns, loaded three adapters ahead, are not waited for (five or
+// six ahead change nothing).
 template <int BM, int THREADS, int FM, int FN>
 __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8_t *lds, int m0, int rows, int row0,
                                  int col0, int N)
