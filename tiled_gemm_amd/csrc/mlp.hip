@@ -23,8 +23,8 @@
 // Measured, both launches: 16 tokens x 4 of 64 experts, 2048 x 1024 gated bf16,
 // pre-shuffled: 95 to 99 us, 5.2 to 5.4 TB/s of 518 MB, a copy's rate.  One token x 8:
 // 26 us (101 MB, 3.8 TB/s: each launch is one or two items per workgroup, start
-// and end included).  61 tokens x 4 of 24, 4096 x 2112 e4m3 as it is: 174 to 177 us,
-// 3.6 TB/s: x and h are read once per item, as many bytes again as the 8-bit
+// and end included).  61 tokens x 4 of 24, 4096 x 2112 e4m3 as it is: 168 to 177 us,
+// 3.5 to 3.7 TB/s: x and h are read once per item, as many bytes again as the 8-bit
 // weights (without those reads 146 us).
 #include "stream.hpp"
 
@@ -121,6 +121,19 @@ constexpr int mlp_red() { return kStreamWaves * 16 * MB * stream_pitch<2>(); }
 template <int MB, bool E8, bool DOWN>
 constexpr int mlp_u() { return MB == 1 && !(E8 && DOWN) ? 2 : 1; }
 
+// A workgroup's first item.  Workgroups go to the XCDs in turn; of every 256 the 32
+// of an XCD take neighbouring items, mostly of one expert, whose rows of x its L2
+// then fetches once.  (Against items in the workgroups' order: 16 tokens x 4 of 64,
+// 2048 x 1024 bf16, pre-shuffled 103 -> 99 us, 64 x 8 as they are 198 -> 189.  With 64 of
+// 512 in a row, so that the two workgroups of a CU are neighbours as well: 104 and
+// 194.)
+__device__ inline int mlp_first()
+{
+    constexpr int kXcds = 8, kRun = 32, kAll = kXcds * kRun;
+    const int b = blockIdx.x, c = b % kAll, at = b - c;
+    return at + kAll > (int)gridDim.x ? b : at + (c % kXcds) * kRun + c / kXcds;
+}
+
 }  // namespace
 
 // x -> h, rows r0 .. of expert e.  Column tile c: the gate's and the linear half's
@@ -186,7 +199,7 @@ __global__ __launch_bounds__(kMlpThreads, 4) void mlp_up_kernel(const MlpArgs a)
             a.done[c] = 0;
     const int active = mlp_mark(sh, a), items = active * a.up_tiles;
     int set = 0;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = mlp_first(); it < items; it += gridDim.x) {
         const int p = it / a.up_tiles, c = it - p * a.up_tiles;
         const int e = mlp_expert(sh, p);
         for (int r0 = 0, cnt = 1; r0 < cnt; r0 += 16 * MB) {
@@ -284,7 +297,7 @@ __global__ __launch_bounds__(kMlpThreads, 4) void mlp_down_kernel(const MlpArgs 
     __shared__ float lds[2][mlp_red<MB>()];
     // Without any active expert the column tiles still have to be written.
     const int active = mlp_mark(sh, a), parts = max(active, 1), items = parts * a.down_tiles;
-    int it = blockIdx.x, r0 = 0, set = 0, stored = -1, counted = -1, reply = 0, turn = 0;
+    int it = mlp_first(), r0 = 0, set = 0, stored = -1, counted = -1, reply = 0, turn = 0;
     while (it < items || stored >= 0 || counted >= 0) {
         int p = 0, c = -1, e = 0, cnt = 0;
         if (it < items) {
