@@ -251,9 +251,11 @@ hipError_t many_mb(const LoraArgs &a, int blocks, hipStream_t s)
 // Parts of K, never less than a step of K per wave.  Few rows: 64 KiB of 16 ranks
 // each.  Many: as many as bring the launch's rounds of workgroups nearest to full
 // (fewest rounds over parts; the LDS of 64 rows by 64 ranks leaves one workgroup
-// per CU, that of the others two or more).  4001 x 4160 and rank 64 in packed
+// per CU, that of 16 or 32 rows two or more).  4001 x 4160 and rank 64 in packed
 // prompts: 22.3 us with the 3 parts that make one round of them, 24.6 with 4;
-// 8000 x 4160 with one adapter 28.3 with 2, 31.0 with 4.
+// 8000 x 4160 with one adapter 28.3 with 2, 31.0 with 4.  64 rows by 32 ranks leave
+// two workgroups per CU, but the tiles read every part: 8192 x 8192 x 2048 takes 326 us
+// in all with 2 parts, 334 with 4.
 int lora_parts(int64_t M, int64_t K, int rank_pad, int adapters)
 {
     const int64_t most = K * 2 / kStepBytes / kStreamWaves;
@@ -264,7 +266,7 @@ int lora_parts(int64_t M, int64_t K, int rank_pad, int adapters)
     }
     const int64_t rows = many_rows(M), passes = rank_pad == 32 ? 1 : (rank_pad + 63) / 64;
     const int64_t wgs = ((M + rows - 1) / rows + more_wgs(adapters, (int)rows)) * passes;
-    const int64_t slots = rows == 64 && rank_pad > 32 ? 256 : 512;
+    const int64_t slots = rows == 64 ? 256 : 512;
     int64_t best = 1, best_rounds = 0;
     for (int64_t p = 1; p <= cap; ++p) {
         const int64_t rounds = (wgs * p + slots - 1) / slots;
