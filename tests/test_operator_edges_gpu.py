@@ -141,6 +141,30 @@ def test_first_half_forms(M, adapters, rank, mix):
     c.check()
 
 
+@pytest.mark.parametrize("layout", ["bt", "bt_preshuffled"])
+@pytest.mark.parametrize("M,kernel,splits", [(5, "auto", 0), (30, "auto", 0), (60, "auto", 0), (100, "auto", 0),
+                                             (700, "auto", 0), (2100, "auto", 0), (300, "generic128", 0),
+                                             (300, "tile256", 0), (300, "tile256", 2)])
+def test_fp32_outputs_get_all_of_v(M, kernel, splits, layout):
+    """Nothing but one product of x and one rank behind each output: v = s (x d), rounded once to fp32, bit for bit."""
+    N, K, rank = 400, 512, 16
+    c = LoraCase(M, N, K, rank, 3, layout=layout, out=torch.float32, kernel=kernel, splits=splits)
+    c.image.zero_()
+    m = torch.arange(M, device="cuda")
+    x = c.a[m, m % K].clone()
+    c.a.zero_()
+    c.a[m, m % K] = x
+    c.up.zero_()
+    n = torch.arange(N, device="cuda")
+    c.up[:, n, n % rank] = 1.0
+    c.run()
+    there = (c.adapter >= 0) & (c.adapter < 3)
+    e = torch.where(there, c.adapter, 0).long()
+    v = c.scale[e][:, None] * (x.float()[:, None] * c.down[e, :, m % K].float())      # (the product of two bf16 is exact)
+    want = torch.where(there[:, None], v, 0.0)[:, n % rank]
+    assert torch.equal(c.c[:M], want) and bool((c.c[M] == 7.0).all())
+
+
 def test_adapters_with_the_planners_split():
     """K above 8192 is split where the plan splits: partial tiles behind v."""
     c = LoraCase(200, 528, 9216, 40, 4, kind="bias_silu", residual=True, preact=True)

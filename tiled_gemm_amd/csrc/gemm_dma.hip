@@ -423,7 +423,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
     // (of a split K the first slice's partial tile takes the adapters' share)
     if constexpr (LORA) {
         if (sk.kt0 == 0)
-            lora_tail<DM_BM, THREADS>(p.lora, acc, lds, m0, rows_a, wm * WTM, n0 + wn * WTN, p.N);
+            lora_tail<DM_BM, THREADS, lora_planes<OUT>()>(p.lora, acc, lds, m0, rows_a, wm * WTM, n0 + wn * WTN, p.N);
     }
 
     // ---- epilogue: row blocks outside, column blocks inside, so a wave

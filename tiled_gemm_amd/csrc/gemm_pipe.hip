@@ -478,7 +478,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
     // (of a split K the first slice's partial tile takes the adapters' share)
     if constexpr (LORA) {
         if (sk.kt0 == 0)
-            lora_tail<BP_BM, 64 * WAVES>(p.lora, acc, lds, m0, rows_a, wm * BP_WTM, n0 + wn * BP_WTN, p.N);
+            lora_tail<BP_BM, 64 * WAVES, lora_planes<OUT>()>(p.lora, acc, lds, m0, rows_a, wm * BP_WTM, n0 + wn * BP_WTN, p.N);
     }
 
     // ---- epilogue: scale, bias, activation, convert, store.  Row blocks

@@ -243,7 +243,7 @@ __global__ __launch_bounds__((64 * skinny_waves<WAVES, LORA>()), 1) void gemm_sk
         if (w < WAVES)
             stream();
         else
-            lora_skinny<MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
+            lora_skinny<lora_planes<OUT>(), MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
     } else {
         stream();
     }
@@ -499,7 +499,7 @@ __global__ __launch_bounds__((64 * skinny_waves<WAVES, LORA>()), 1) void gemm_sk
         if (w < WAVES)
             stream();
         else
-            lora_skinny<MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
+            lora_skinny<lora_planes<OUT>(), MB, NB>(p.lora, acc, p.M, p.N, n0, w - WAVES, kLoraWaves);
     } else {
         stream();
     }

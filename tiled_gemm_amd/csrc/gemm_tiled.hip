@@ -340,9 +340,9 @@ __global__ __launch_bounds__(kTiledThreads, LORA && NS == 2 ? 2 : 1) void gemm_t
     const uint32_t ldc = (uint32_t)p.N * OB;
     const auto rC = make_rsrc((uint8_t *)p.C + (size_t)m0 * ldc, (uint32_t)rows_a * ldc);
     const EpiExt ex = EX ? epi_ext(p.epi, (size_t)m0 * ldc, (uint32_t)rows_a * ldc) : EpiExt{};
-    static_assert(!LORA || lora_lds_bytes<BM>() <= Cfg::LDS, "v fits the stages");
+    static_assert(!LORA || lora_lds_bytes<BM, lora_planes<OUT>()>() <= Cfg::LDS, "v fits the stages");
     if constexpr (LORA)
-        lora_tail<BM, kTiledThreads>(p.lora, acc, lds, m0, rows_a, wm * Cfg::WTM, n0 + wn * Cfg::WTN, p.N);
+        lora_tail<BM, kTiledThreads, lora_planes<OUT>()>(p.lora, acc, lds, m0, rows_a, wm * Cfg::WTM, n0 + wn * Cfg::WTN, p.N);
     if constexpr (EX) {
         constexpr int EB = Cfg::EB;
         __syncthreads();                       // every wave has read its last fragments before LDS is reused

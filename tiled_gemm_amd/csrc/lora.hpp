@@ -10,10 +10,11 @@
 // (Choosing the finished sums rather than clearing the other rows' v keeps an
 // infinity or NaN of one adapter's matrices out of the other adapters' rows.)
 //
-// v goes to the matrix unit as two bf16 numbers, v = hi + lo within 2^-17 of it,
-// for twice the MFMAs of a product that is 1 to 3% of the projection's: rounding
-// v to one bf16 would add an error as large as the output's own rounding where
-// the adapters' share of z is large.  v comes as fp32 partial sums over parts of
+// v goes to the matrix unit as a sum of bf16 numbers, for as many MFMAs of a
+// product that is 1 to 3% of the projection's: of two (within 2^-17) where the
+// output is bf16, as rounding v to one would add an error as large as the
+// output's own rounding where the adapters' share of z is large; of three (within
+// 2^-24) where it is fp32 or an fp32 partial tile.  v comes as fp32 partial sums over parts of
 // K, which the reader adds.
 #pragma once
 
@@ -21,15 +22,23 @@
 
 namespace tg {
 
-// Eight fp32 numbers as bf16 operands hi + lo.
-__device__ inline void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 &hi, u32x4 &lo)
+// bf16 numbers that stand for one of v.
+template <int OUT>
+constexpr int lora_planes() { return OUT == kOutF32 ? 3 : 2; }
+
+// Eight fp32 numbers as the sums of P bf16 operands.
+template <int P>
+__device__ inline void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 (&o)[P])
 {
-    const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        hi[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-        lo[i] = pack_bf16x2(v[2 * i] - bf16_lo(hi[i]), v[2 * i + 1] - bf16_hi(hi[i]));
-    }
+    for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[p][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+            v[2 * i] -= bf16_lo(o[p][i]);
+            v[2 * i + 1] -= bf16_hi(o[p][i]);
+        }
 }
 
 // This lane's place among the columns of `up`: its row r16 of each column block
@@ -62,9 +71,8 @@ struct LoraCols {
 
 // acc += v b^T for the rows whose bit is set in `same` (bit 16 i + r: row r of
 // block i), 32 ranks.
-template <int CH, int FN>
-__device__ inline void lora_add(f32x4 (*acc)[FN], const u32x4 (&hi)[CH], const u32x4 (&lo)[CH], const u32x4 (&b)[FN],
-                                unsigned long long same)
+template <int P, int CH, int FN>
+__device__ inline void lora_add(f32x4 (*acc)[FN], const u32x4 (&v)[CH][P], const u32x4 (&b)[FN], unsigned long long same)
 {
     const int r16 = lane_id() & 15;
 #pragma unroll
@@ -74,8 +82,10 @@ __device__ inline void lora_add(f32x4 (*acc)[FN], const u32x4 (&hi)[CH], const u
         const bool mine = (same >> (i * 16 + r16)) & 1;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-            f32x4 t = mfma_bf16(b[j], hi[i], f32x4{0.f, 0.f, 0.f, 0.f});
-            t = mfma_bf16(b[j], lo[i], t);
+            f32x4 t = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                t = mfma_bf16(b[j], v[i][p], t);
 #pragma unroll
             for (int c = 0; c < 4; ++c)
                 acc[i][j][c] += mine ? t[c] : 0.f;
@@ -113,25 +123,26 @@ __device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, f32x4 &a, 
     }
 }
 
-// LDS of lora_tail: 32 ranks of the tile's rows, hi and lo.
-template <int BM>
-constexpr int lora_lds_bytes() { return BM * 128; }
+// LDS of lora_tail: 32 ranks of the tile's rows, P times.
+template <int BM, int P>
+constexpr int lora_lds_bytes() { return BM * 64 * P; }
 
 // acc[i][j] of a tile wave: row block i holds the tile's rows row0 + 16 i .., of
 // which `rows` exist, from row m0 of C on.  All waves of the tile's workgroup
 // call it: v goes through LDS, so that it is read, added up and split once per
 // tile and not once per wave (with the parts of K that are added up here:
 // 8192 x 8192 x 2048, rank 32, 337 -> 328 us).  LDS may still be read by other waves
-// before the call and after it.  What it costs: about 3 us per tile (that shape:
-// 13 us of 328 in four rounds of tiles), and some 250 cycles for each adapter
-// beyond the first among a wave's 64 rows, a chain of ballots and two dependent
-// MFMAs; their columns, loaded three adapters ahead, are not waited for (five or
-// six ahead change nothing).
-template <int BM, int THREADS, int FM, int FN>
+// before the call and after it.  What it costs with one adapter is hard to see
+// (that shape's kernel: 287 us, 286 without adapters; 2000 x 4096 x 4160, rank 64: 103
+// and 98); each adapter beyond the first among a wave's 64 rows takes some 250
+// cycles, a chain of ballots and dependent MFMAs.  Their columns, loaded three
+// adapters ahead, are not waited for (five or six ahead change nothing).
+template <int BM, int THREADS, int P, int FM, int FN>
 __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8_t *lds, int m0, int rows, int row0,
                                  int col0, int N)
 {
-    constexpr int CH = FM < 4 ? FM : 4;              // row blocks at a time: a row per lane
+    // Row blocks at a time: a row per lane, and what the registers hold.
+    constexpr int MOST = P == 2 ? 4 : 2, CH = FM < MOST ? FM : MOST;
     constexpr int CHUNKS = FM / CH;
     static_assert(FM % CH == 0, "whole chunks");
     const int l = lane_id(), q = l >> 4, r16 = l & 15;
@@ -141,7 +152,6 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
         const int row = row0 + 16 * CH * c + l;
         id[c] = lora_id(lo, l < 16 * CH && row < rows, m0 + row);
     }
-    uint8_t *const lds_hi = lds, *const lds_lo = lds + BM * 64;
     for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
         const LoraCols<FN> cols(lo, N, col0, r0);
         __syncthreads();
@@ -150,10 +160,11 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
             if (row < rows)
                 lora_v8(lo, (size_t)(m0 + row), r0 + 8 * c, va, vb);
-            u32x4 hi, low;
-            split_bf16(va, vb, hi, low);
-            *(u32x4 *)(lds_hi + it * 16) = hi;
-            *(u32x4 *)(lds_lo + it * 16) = low;
+            u32x4 o[P];
+            split_bf16<P>(va, vb, o);
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+                *(u32x4 *)(lds + p * BM * 64 + it * 16) = o[p];
         }
         __syncthreads();
         u32x4 b[3][FN];
@@ -175,13 +186,12 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
                 cols.load(lo, e0, b[0]);
             if (e1 >= 0)
                 cols.load(lo, e1, b[1]);
-            u32x4 hi[CH], low[CH];
+            u32x4 v[CH][P];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int at = (row0 + 16 * (C * CH + i) + r16) * 64 + q * 16;
-                hi[i] = lds_load16(lds_hi + at);
-                low[i] = lds_load16(lds_lo + at);
-            }
+            for (int i = 0; i < CH; ++i)
+#pragma unroll
+                for (int p = 0; p < P; ++p)
+                    v[i][p] = lds_load16(lds + p * BM * 64 + (row0 + 16 * (C * CH + i) + r16) * 64 + q * 16);
             // One adapter's products from `now` while the columns of the one after
             // the next start on their way to `ahead` (a decode row's adapter has
             // not been read before: its columns come from HBM); false after the last.
@@ -192,7 +202,7 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
                 e1 = pop();
                 if (e1 >= 0)
                     cols.load(lo, e1, ahead);
-                lora_add<CH, FN>(&acc[C * CH], hi, low, now, same);
+                lora_add<P, CH, FN>(&acc[C * CH], v, now, same);
                 return e0 >= 0;
             };
             while (one(b[0], b[2])) {
@@ -210,7 +220,7 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
 // The same for a few rows (M <= 64), the adapters shared out to `waves` waves:
 // wave w of them takes every waves-th that occurs.  acc: sums to be added to the
 // other waves'.
-template <int MB, int FN>
+template <int P, int MB, int FN>
 __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int M, int N, int col0, int w, int waves)
 {
     const int l = lane_id(), q = l >> 4, r16 = l & 15;
@@ -238,19 +248,19 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
             return;                                  // fewer adapters than waves
         u32x4 b[FN], b1[FN];
         cols.load(lo, e, b);
-        u32x4 hi[MB], low[MB];
+        u32x4 v[MB][P];
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
             if (16 * i + r16 < M)
                 lora_v8(lo, 16 * i + r16, r0 + 8 * q, va, vb);
-            split_bf16(va, vb, hi[i], low[i]);
+            split_bf16<P>(va, vb, v[i]);
         }
         while (e >= 0) {
             const int e1 = next(&same1);
             if (e1 >= 0)
                 cols.load(lo, e1, b1);               // in flight while this one's products run
-            lora_add<MB, FN>(acc, hi, low, b, same);
+            lora_add<P, MB, FN>(acc, v, b, same);
             e = e1;
             same = same1;
 #pragma unroll
