@@ -21,7 +21,7 @@
 //     last adds the slots of every token in the order of j.  Which workgroup that
 //     is does not change the result.
 // Measured, both launches: 16 tokens x 4 of 64 experts, 2048 x 1024 gated bf16,
-// pre-shuffled: 95 to 99 us, 5.2 to 5.4 TB/s of 518 MB, a copy's rate.  One token x 8:
+// pre-shuffled: 90 to 99 us, 5.2 to 5.7 TB/s of 518 MB, a copy's rate.  One token x 8:
 // 26 us (101 MB, 3.8 TB/s: each launch is one or two items per workgroup, start
 // and end included).  61 tokens x 4 of 24, 4096 x 2112 e4m3 as it is: 168 to 177 us,
 // 3.5 to 3.7 TB/s: x and h are read once per item, as many bytes again as the 8-bit
