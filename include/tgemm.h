@@ -343,8 +343,8 @@ int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, voi
  *   C[m][n] = cvt( act(z[m][n])  (+ residual[m][n]) )          preact[m][n] = cvt( z[m][n] )
  *
  * Both sums over r and k are fp32; v is not rounded to bf16 (it enters the
- * second product as a sum of two bf16 numbers, within 2^-17 of it, or of three,
- * within 2^-24, where the output is fp32).  A row whose adapter is outside
+ * second product as a sum of two bf16 numbers, within 2^-16 of it, or of three,
+ * within 2^-24, where the output is fp32; an infinite v stays one).  A row whose adapter is outside
  * 0 .. adapters - 1 has none.  Rows of different adapters may be mixed in any
  * order; an adapter's infinities and NaN reach its own rows only.
  *   adapter  device pointer, M ints;

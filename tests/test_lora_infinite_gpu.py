@@ -1,0 +1,93 @@
+"""Low-rank adapters whose sums leave the finite numbers: where the definition
+
+    v = scale sum_k x down,   z = x B^T + sum_r v up
+
+gives an infinity, z is that infinity and not NaN (which ReLU would turn into 0),
+whatever the kernel makes of v on the way.
+"""
+import pytest
+import torch
+
+from test_lora_gpu import Case
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+INF = float("inf")
+
+# (M, kernel, splits): the skinny kernels, small and large tiles, split K
+FORMS = [(5, "auto", 0), (40, "auto", 0), (64, "auto", 0), (100, "auto", 0), (300, "auto", 0), (300, "generic128", 0),
+         (300, "tile256", 0), (300, "tile256", 2)]
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    yield
+
+
+def make(form, layout="bt", out=BF16, kind="none", rank=16, K=512, **kw):
+    M, kernel, splits = form
+    c = Case(M, 96, K, rank, 3, layout, out, kind, kernel=kernel, splits=splits, **kw)
+    c.adapter.copy_((torch.arange(M, device="cuda") % 4 - 1).to(torch.int32))
+    return c
+
+
+def rows_of(c, e=1):
+    return torch.nonzero(c.adapter == e).flatten()
+
+
+def same(got, want):
+    """Equal, infinities and NaN included."""
+    got, want = got.double(), want.double()
+    return torch.equal(torch.isnan(got), torch.isnan(want)) and \
+        torch.equal(got[~torch.isnan(want)], want[~torch.isnan(want)])
+
+
+@pytest.mark.parametrize("layout", ["bt", "bt_preshuffled"])
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("kind", ["none", "bias_relu"])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_v(form, kind, out, layout):
+    """One infinite element of down behind a nonzero x: z is an infinity of the sign of up."""
+    c = make(form, layout, out, kind, preact=True)
+    c.a[:, 5] = 1.0
+    c.down[1, 3, 5] = INF
+    sign = torch.where(torch.arange(96, device="cuda") % 3 == 0, -1.0, 1.0)
+    c.up[1, :, 3] = (sign * 0.75).to(BF16)
+    c.run()
+    rows = rows_of(c)
+    want = (sign * INF).expand(rows.numel(), 96)
+    assert same(c.z[rows], want)
+    assert same(c.c[rows], want.clamp(min=0) if kind == "bias_relu" else want)
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_up(form, out):
+    """An infinite element of up: that column is an infinity of the sign of v."""
+    c = make(form, out=out)
+    c.a[:, 6:] = 0.0                                  # v of bf16 products: some have no lower bits at all
+    c.down[1, 2] = 0.0
+    c.a[:, 4] = torch.where(torch.arange(form[0], device="cuda") % 8 < 4, 1.0, -3.0).to(BF16)
+    c.down[1, 2, 4] = 0.5
+    c.up[1, 7, 2] = -INF
+    c.run()
+    rows = rows_of(c)
+    assert same(c.c[rows, 7], -INF * c.a[rows, 4].double())
+    assert bool(torch.isfinite(c.c[rows][:, torch.arange(96, device="cuda") != 7].float()).all())
+
+
+@pytest.mark.parametrize("out", [BF16, F32])
+@pytest.mark.parametrize("form", FORMS)
+def test_v_above_the_largest_bf16(form, out):
+    """A finite v that a bf16 number cannot hold: z within the usual tolerance."""
+    c = make(form, out=out)
+    c.b[:, 5], c.down[:, :, 5], c.up[1, :, 3] = 0.0, 0.0, c.up[1, :, 3] * 2.0 ** -100
+    c.a[:, 5], c.down[1, 3], c.down[1, 3, 5] = 2.0 ** 120, 0.0, 1.0
+    c.scale[1] = (2.0 - 2.0 ** -12) * 2.0 ** 7        # v = (2 - 2^-12) 2^127; 2^128 in bf16
+    c.scale[0] = c.scale[2] = 1.0
+    c.up[1, :, [i for i in range(16) if i != 3]] = 0.0
+    c.run()
+    torch.cuda.synchronize()
+    c.check()

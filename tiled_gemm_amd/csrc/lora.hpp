@@ -11,7 +11,7 @@
 // infinity or NaN of one adapter's matrices out of the other adapters' rows.)
 //
 // v goes to the matrix unit as a sum of bf16 numbers, for as many MFMAs of a
-// product that is 1 to 3% of the projection's: of two (within 2^-17) where the
+// product that is 1 to 3% of the projection's: of two (within 2^-16) where the
 // output is bf16, as rounding v to one would add an error as large as the
 // output's own rounding where the adapters' share of z is large; of three (within
 // 2^-24) where it is fp32 or an fp32 partial tile.  v comes as fp32 partial sums over parts of
@@ -26,19 +26,31 @@ namespace tg {
 template <int OUT>
 constexpr int lora_planes() { return OUT == kOutF32 ? 3 : 2; }
 
-// Eight fp32 numbers as the sums of P bf16 operands.
+// Eight fp32 numbers as the sums of P bf16 operands: each but the last cuts the
+// number off after 8 bits, so what is left has the number's sign, and where
+// nothing is left 2^-28 of the number follows, which no fp32 sum beside the number
+// holds.  So the operands are infinite, NaN, zero or of one sign together, and
+// against an infinite element of `up` their products are one infinity (while |v| is
+// above 2^-105, where 2^-28 of it is still a number).  Rounded to nearest instead, the
+// remainder of an infinity is NaN, and any other may have the other sign or be zero:
+// NaN for an infinite z.  (No slower, either: 150 / 150 us in packed prompts; a check
+// of every product for infinities took 160.)
 template <int P>
 __device__ inline void split_bf16(const f32x4 &a, const f32x4 &b, u32x4 (&o)[P])
 {
     float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P - 1; ++p)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            o[p][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
-            v[2 * i] -= bf16_lo(o[p][i]);
-            v[2 * i + 1] -= bf16_hi(o[p][i]);
+            const uint32_t lo = __builtin_bit_cast(uint32_t, v[2 * i]), hi = __builtin_bit_cast(uint32_t, v[2 * i + 1]);
+            o[p][i] = lo >> 16 | (hi & 0xFFFF0000u);
+            v[2 * i] = lo & 0xFFFF ? v[2 * i] - bf16_lo(o[p][i]) : v[2 * i] * 0x1p-28f;
+            v[2 * i + 1] = hi & 0xFFFF ? v[2 * i + 1] - bf16_hi(o[p][i]) : v[2 * i + 1] * 0x1p-28f;
         }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        o[P - 1][i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
 }
 
 // This lane's place among the columns of `up`: its row r16 of each column block
