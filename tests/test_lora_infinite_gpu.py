@@ -91,3 +91,17 @@ def test_v_above_the_largest_bf16(form, out):
     c.run()
     torch.cuda.synchronize()
     c.check()
+
+
+@pytest.mark.parametrize("rank", [8, 40])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_x_and_padded_ranks(form, rank):
+    """Ranks that fill up a block of 32 have no part in z: an infinite x with positive weights gives an infinity."""
+    c = make(form, rank=rank, kind="bias_relu")
+    m = form[0] // 2
+    e = max(int(c.adapter[m]), 0)
+    c.adapter[m] = e
+    c.a[m, 5] = INF
+    c.b[:, 5], c.down[e, :, 5], c.up[e] = 0.5, 0.25, c.up[e].abs() + 0.125
+    c.run()
+    assert bool((c.c[m] == INF).all())

@@ -48,7 +48,7 @@ struct LoraArgs {
     const void *up;             // adapters x N x rank bf16
     const float *scale;         // nullptr (1) or one per adapter
     int32_t adapters, rank;
-    int32_t rank_pad;           // rank rounded up to 32 (the rest of v is zeros)
+    int32_t rank_pad;           // rank rounded up to 32: v's pitch (the rest of a row is not used)
     int32_t M, K;
     int32_t parts;              // partial sums over K, lora_parts()
 };

@@ -102,7 +102,7 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, unsigned long long t
     __syncthreads();
     for (int o = threadIdx.x; o < 16 * MB * 16 * NB; o += kStreamThreads) {
         const int row = o / (16 * NB), col = o % (16 * NB), r = rb * 16 * NB + col;
-        if (!((same >> row) & 1) || r >= a.rank_pad)
+        if (!((same >> row) & 1) || r >= a.rank)
             continue;
         a.v[((size_t)part * a.M + m0 + row) * a.rank_pad + r] = s * stream_sum<MB, NB>(red, row, col);
     }

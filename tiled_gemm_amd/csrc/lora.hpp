@@ -113,6 +113,9 @@ __device__ inline int lora_id(const LoraArgs &lo, bool there, int row)
 }
 
 // Eight ranks of a row of v from column c on: its parts added, in their order.
+// (Ranks past the last, up to a multiple of 32, are zeros to the matrix unit; they
+// are neither stored nor read: an infinite x times the zeros that its rows of
+// `down` would be is NaN.)
 __device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, f32x4 &a, f32x4 &b)
 {
     const float *const p = (const float *)lo.v + row * lo.rank_pad + c;
@@ -170,7 +173,7 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
         for (int it = threadIdx.x; it < BM * 4; it += THREADS) {
             const int row = it >> 2, c = it & 3;
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
-            if (row < rows)
+            if (row < rows && r0 + 8 * c < lo.rank)
                 lora_v8(lo, (size_t)(m0 + row), r0 + 8 * c, va, vb);
             u32x4 o[P];
             split_bf16<P>(va, vb, o);
@@ -264,7 +267,7 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
 #pragma unroll
         for (int i = 0; i < MB; ++i) {
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
-            if (16 * i + r16 < M)
+            if (16 * i + r16 < M && r0 + 8 * q < lo.rank)
                 lora_v8(lo, 16 * i + r16, r0 + 8 * q, va, vb);
             split_bf16<P>(va, vb, v[i]);
         }
