@@ -105,3 +105,31 @@ def test_infinite_x_and_padded_ranks(form, rank):
     c.b[:, 5], c.down[e, :, 5], c.up[e] = 0.5, 0.25, c.up[e].abs() + 0.125
     c.run()
     assert bool((c.c[m] == INF).all())
+
+
+@pytest.mark.parametrize("form", FORMS + [(2100, "auto", 0)])
+def test_infinite_scale_and_parts_of_k(form):
+    """The scale multiplies the whole sum, not parts of it that differ in sign or are zero."""
+    K = 8192
+    c = make(form, K=K)
+    c.a.zero_()
+    c.a[:, 0], c.a[:, K // 2], c.a[:, K - 1] = 1.0, 1.0, 1.0
+    c.down[1, :, 0], c.down[1, :, K // 2], c.down[1, :, K - 1] = -1.0, -1.0, 4.0       # sum 2
+    c.up[1] = c.up[1].abs() + 0.125
+    c.scale[1] = INF
+    c.run()
+    rows = rows_of(c)
+    assert bool((c.c[rows] == INF).all())
+    # and a finite scale whose products with the parts overflow: v = 2^111
+    c.a[:, 0] = c.a[:, K - 1] = 2.0 ** 20
+    c.b[:, 0] = c.b[:, K - 1] = 0.0
+    c.down[:, :, 0], c.down[:, :, K - 1] = -1.0, 1.0
+    c.down[:, :, K // 2] = 2.0
+    c.scale.fill_(2.0 ** 110)
+    c.up.copy_(torch.where(c.up == 0, 1.0, torch.sign(c.up.float())) * 2.0 ** -110)
+    c.run()
+    rows = torch.nonzero(c.adapter >= 0).flatten()
+    e = c.adapter[rows].long()
+    want = c.a[rows].double() @ c.b.double().t().contiguous() + 2.0 * 2.0 ** 110 * c.up.double().sum(dim=2)[e]
+    # (sums of small integers and of x B's one product a column; one rounding of the output and of the sum)
+    assert bool(((c.c[rows].double() - want).abs() <= (2.0 ** -8 + 2.0 ** -20) * want.abs() + 2.0 ** -18).all())

@@ -1,8 +1,9 @@
 // Low-rank adapters of many requests, the first half:
 //
-//   v[m][r] = s_a sum_k x[m][k] down_a[r][k],     a the adapter of row m
+//   v[m][r] / s_a = sum_k x[m][k] down_a[r][k],     a the adapter of row m
 //
-// for the projection's kernel to finish (lora.hpp): fp32 sums over parts of K.
+// for the projection's kernel to finish (lora.hpp), which also scales: fp32 sums
+// over parts of K.
 //
 // A CU alone streams some 30 to 50 GB/s, so what counts is the bytes that each
 // workgroup reads and that there are enough workgroups: K is cut into parts (up
@@ -82,10 +83,8 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, unsigned long long t
     for (int i = 0; i < MB; ++i)                     // (rows past M are past the record count)
         xoff[i] = keep_or_oob((there >> (i * 16 + r16)) & 1, (uint32_t)(i * 16 + r16) * kb);
     unsigned long long same = 0;
-    float s = 1.f;
     auto find = [&](__amdgpu_buffer_rsrc_t (&rB)[NB]) {
         const int e = find_adapter(&same), any = e < 0 ? 0 : e;
-        s = a.scale ? a.scale[any] : 1.f;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             // ranks past the last (of a padded block) read zeros
@@ -104,7 +103,7 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, unsigned long long t
         const int row = o / (16 * NB), col = o % (16 * NB), r = rb * 16 * NB + col;
         if (!((same >> row) & 1) || r >= a.rank)
             continue;
-        a.v[((size_t)part * a.M + m0 + row) * a.rank_pad + r] = s * stream_sum<MB, NB>(red, row, col);
+        a.v[((size_t)part * a.M + m0 + row) * a.rank_pad + r] = stream_sum<MB, NB>(red, row, col);
     }
 }
 

@@ -1,5 +1,5 @@
 // Low-rank adapters beside a shared projection: the second half, inside the
-// projection's kernel (the first half, v = s x down^T, is lora.hip).
+// projection's kernel (the first half, v / s = x down^T, is lora.hip).
 //
 //   z[m][n] = sum_k x[m][k] b[n][k] + sum_r v[m][r] up_a[n][r],     a the adapter of row m
 //
@@ -112,11 +112,21 @@ __device__ inline int lora_id(const LoraArgs &lo, bool there, int row)
     return (uint32_t)id < (uint32_t)lo.adapters ? id : -1;
 }
 
-// Eight ranks of a row of v from column c on: its parts added, in their order.
+// The factor of a row with the adapter `id` (any, where it has none: its v is not used).
+__device__ inline float lora_scale(const LoraArgs &lo, int id)
+{
+    return lo.scale ? lo.scale[(uint32_t)id < (uint32_t)lo.adapters ? id : 0] : 1.f;
+}
+
+// Eight ranks of a row of v from column c on: its parts added, in their order, and
+// scaled.  (The parts one by one would make NaN of an infinite scale where they
+// differ in sign or are zero, and of a large one whose products with them
+// overflow.  Reading the scale here costs 32 decode rows 0.8 of 36 us, tiles nothing
+// that shows.)
 // (Ranks past the last, up to a multiple of 32, are zeros to the matrix unit; they
 // are neither stored nor read: an infinite x times the zeros that its rows of
 // `down` would be is NaN.)
-__device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, f32x4 &a, f32x4 &b)
+__device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, float scale, f32x4 &a, f32x4 &b)
 {
     const float *const p = (const float *)lo.v + row * lo.rank_pad + c;
     const size_t part = (size_t)lo.M * lo.rank_pad;
@@ -136,6 +146,8 @@ __device__ inline void lora_v8(const LoraArgs &lo, size_t row, int c, f32x4 &a, 
             b += y[s];
         }
     }
+    a *= scale;
+    b *= scale;
 }
 
 // LDS of lora_tail: 32 ranks of the tile's rows, P times.
@@ -167,14 +179,23 @@ __device__ inline void lora_tail(const LoraArgs &lo, f32x4 (&acc)[FM][FN], uint8
         const int row = row0 + 16 * CH * c + l;
         id[c] = lora_id(lo, l < 16 * CH && row < rows, m0 + row);
     }
+    constexpr int ITEMS = BM * 4 / THREADS;
+    static_assert(BM * 4 % THREADS == 0, "as many pieces of v for every thread");
+    float scale[ITEMS];
+#pragma unroll
+    for (int u = 0; u < ITEMS; ++u) {
+        const int row = (threadIdx.x + u * THREADS) >> 2;
+        scale[u] = lora_scale(lo, lo.adapter[m0 + min(row, rows - 1)]);
+    }
     for (int r0 = 0; r0 < lo.rank_pad; r0 += 32) {
         const LoraCols<FN> cols(lo, N, col0, r0);
         __syncthreads();
-        for (int it = threadIdx.x; it < BM * 4; it += THREADS) {
-            const int row = it >> 2, c = it & 3;
+#pragma unroll
+        for (int u = 0; u < ITEMS; ++u) {
+            const int it = threadIdx.x + u * THREADS, row = it >> 2, c = it & 3;
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
             if (row < rows && r0 + 8 * c < lo.rank)
-                lora_v8(lo, (size_t)(m0 + row), r0 + 8 * c, va, vb);
+                lora_v8(lo, (size_t)(m0 + row), r0 + 8 * c, scale[u], va, vb);
             u32x4 o[P];
             split_bf16<P>(va, vb, o);
 #pragma unroll
@@ -240,6 +261,10 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
 {
     const int l = lane_id(), q = l >> 4, r16 = l & 15;
     const int id = lora_id(lo, l < M, l);
+    float scale[MB];
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+        scale[i] = lora_scale(lo, lo.adapter[min(16 * i + r16, M - 1)]);
     // The wave's next adapter: its first row's, every waves-th of those left.
     unsigned long long left = 0;
     int n = 0;
@@ -268,7 +293,7 @@ __device__ inline void lora_skinny(const LoraArgs &lo, f32x4 (&acc)[MB][FN], int
         for (int i = 0; i < MB; ++i) {
             f32x4 va = {0.f, 0.f, 0.f, 0.f}, vb = va;
             if (16 * i + r16 < M && r0 + 8 * q < lo.rank)
-                lora_v8(lo, 16 * i + r16, r0 + 8 * q, va, vb);
+                lora_v8(lo, 16 * i + r16, r0 + 8 * q, scale[i], va, vb);
             split_bf16<P>(va, vb, v[i]);
         }
         while (e >= 0) {
