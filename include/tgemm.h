@@ -361,6 +361,8 @@ int gemm_run_ws_noalloc(const gemm_plan *plan, const void *A, const void *B, voi
  *            where K is split: above 8192 where the plan splits, and where its
  *            options say so).  Calls that share one must not overlap
  *            in time.
+ * The workspace, C and preact overlap no other operand, the bias among them
+ * (but C may be the residual).
  * Asynchronous; allocates nothing; two launches (three with split K).  GEMM_OK
  * or an error.
  */

@@ -1,0 +1,21 @@
+"""Refusals of the adapters and of the few-token expert layer that come before anything is launched, on the CPU."""
+import pytest
+
+import tiled_gemm_amd as tg
+
+BF, BT, PRE = tg.GEMM_BF16_OUT_BF16, tg.LAYOUTS["bt"], tg.LAYOUTS["bt_preshuffled"]
+P = 1 << 40                     # an aligned address that is never read
+AT = [P + (i << 34) for i in range(12)]
+
+
+@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("change", [dict(workspace=AT[10]), dict(C=AT[10]), dict(preact=AT[10]),
+                                    dict(workspace=AT[10] + 240), dict(C=AT[10] + 240)])
+def test_adapters_bias_overlaps_an_output(M, change):
+    """The bias is read behind the first launch, which has written the workspace by then."""
+    a = dict(A=AT[0], B=AT[1], C=AT[2], adapter=AT[3], adapters=4, rank=16, down=AT[4], up=AT[5], scale=AT[6],
+             residual=AT[7], preact=AT[8], workspace=AT[9], workspace_bytes=1 << 33, bias=AT[10],
+             epilogue=tg.GEMM_EPI_BIAS)
+    a.update(change)
+    with tg.Plan(M, 64, 128, BF, BT) as p, pytest.raises(tg.GemmError, match="overlap"):
+        p.run_lora(**a)

@@ -1127,7 +1127,7 @@ int gemm_run_lora(const gemm_plan *plan, const void *A, const void *B, void *C, 
         size_t n;
     } in[] = {{A, (size_t)I.M * plan->kbytes}, {B, (size_t)I.N * plan->kbytes_b}, {lora->adapter, (size_t)I.M * 4},
               {lora->down, n * (size_t)I.K},   {lora->up, n * (size_t)I.N},       {lora->scale, (size_t)lora->adapters * 4},
-              {residual, residual == C ? 0 : cbytes}};
+              {residual, residual == C ? 0 : cbytes}, {e.bias, (size_t)I.N * 4}};
     using tg::capi_overlap;
     for (const auto &v : in)
         if (capi_overlap(workspace, need, v.p, v.n) || capi_overlap(C, cbytes, v.p, v.n) ||
