@@ -694,8 +694,10 @@ size_t gemm_group_mlp_workspace_bytes(const gemm_group_mlp_plan *plan);
 
 /*
  * gemm_group_mlp_preshuffle -- the pre-shuffled images of both matrices (each
- * as large as its source; gemm_group_preshuffle_b on each, whose errors it
- * has).  For plans with GEMM_LAYOUT_BT_PRESHUFFLED.
+ * as large as its source; gemm_group_preshuffle_b on each).  All four are
+ * 16-byte aligned, the images overlap neither a matrix nor each other, and
+ * nothing is launched where one is refused.  For plans with
+ * GEMM_LAYOUT_BT_PRESHUFFLED.
  */
 int gemm_group_mlp_preshuffle(const gemm_group_mlp_plan *plan, const void *up, void *up_image, const void *down,
                               void *down_image, hipStream_t stream);

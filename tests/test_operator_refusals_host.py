@@ -19,3 +19,16 @@ def test_adapters_bias_overlaps_an_output(M, change):
     a.update(change)
     with tg.Plan(M, 64, 128, BF, BT) as p, pytest.raises(tg.GemmError, match="overlap"):
         p.run_lora(**a)
+
+
+@pytest.mark.parametrize("change,why", [
+    (dict(down=0), "NULL"), (dict(down_image=0), "NULL"), (dict(down=AT[2] + 8), "16-byte"),
+    (dict(down_image=AT[3] + 4), "16-byte"), (dict(down_image=AT[2] + 16), "overlap"), (dict(down_image=AT[1]), "overlap"),
+    (dict(down_image=AT[0]), "overlap"), (dict(up_image=AT[2]), "overlap"), (dict(up_image=AT[3] + 4096), "overlap")])
+def test_preshuffle_checks_both_matrices_first(change, why):
+    """Nothing is launched for one matrix where the other is refused, and no image lies on what is still to be read."""
+    a = dict(up=AT[0], up_image=AT[1], down=AT[2], down_image=AT[3])
+    a.update(change)
+    with tg.GroupMlpPlan(8, 4, 2, 128, 64, tg.GEMM_TYPE_BF16, PRE, True, tg.GEMM_EPI_BIAS_SILU) as p, \
+            pytest.raises(tg.GemmError, match=why):
+        p.preshuffle(**a)

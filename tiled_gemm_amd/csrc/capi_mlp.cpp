@@ -142,6 +142,16 @@ int gemm_group_mlp_preshuffle(const gemm_group_mlp_plan *plan, const void *up, v
 {
     if (!plan)
         return capi_fail(GEMM_ERR_INVALID_ARG, "NULL plan");
+    // Both matrices' checks come before the first launch.
+    if (!up || !up_image || !down || !down_image)
+        return capi_fail(GEMM_ERR_INVALID_ARG, "NULL up, up_image, down or down_image");
+    if (!capi_aligned(up, 16) || !capi_aligned(up_image, 16) || !capi_aligned(down, 16) || !capi_aligned(down_image, 16))
+        return capi_fail(GEMM_ERR_INVALID_ARG, "up, down and their images must be 16-byte aligned");
+    const size_t ub = gemm_group_preshuffled_b_bytes(plan->up), db = gemm_group_preshuffled_b_bytes(plan->down);
+    if (capi_overlap(up_image, ub, up, ub) || capi_overlap(up_image, ub, down, db) ||
+        capi_overlap(down_image, db, up, ub) || capi_overlap(down_image, db, down, db) ||
+        capi_overlap(up_image, ub, down_image, db))
+        return capi_fail(GEMM_ERR_INVALID_ARG, "an image overlaps a matrix or the other image");
     if (int rc = gemm_group_preshuffle_b(plan->up, up, up_image, stream))
         return rc;
     return gemm_group_preshuffle_b(plan->down, down, down_image, stream);
