@@ -660,7 +660,9 @@ int gemm_group_combine_grad(int64_t tokens, int topk, int64_t N, int type, const
  * order of j, the residual last.  A slot whose id is outside 0 .. groups - 1
  * contributes nothing (nor is its weight read as a factor).  The result does
  * not depend on scheduling: every run gives the same bits.  For more tokens
- * use gemm_group_sort, gemm_group_run and gemm_group_combine.
+ * there are gemm_group_sort, gemm_group_run and gemm_group_combine: without the
+ * gate's product, which is the caller's between two runs, and with rows of the
+ * weights' type (e4m3 beside e4m3 weights).
  *
  * gemm_group_mlp_plan_create
  *   groups   1 .. GEMM_GROUP_MAX;  tokens 0 .. GEMM_GROUP_MLP_MAX_TOKENS;

@@ -32,3 +32,14 @@ def test_preshuffle_checks_both_matrices_first(change, why):
     with tg.GroupMlpPlan(8, 4, 2, 128, 64, tg.GEMM_TYPE_BF16, PRE, True, tg.GEMM_EPI_BIAS_SILU) as p, \
             pytest.raises(tg.GemmError, match=why):
         p.preshuffle(**a)
+
+
+@pytest.mark.parametrize("gated,weight_type", [(True, tg.GEMM_TYPE_BF16), (False, tg.GEMM_TYPE_BF16),
+                                               (True, tg.GEMM_TYPE_E4M3), (False, tg.GEMM_TYPE_E4M3)])
+def test_more_tokens_than_the_layer_takes(gated, weight_type):
+    """The refusal names the single products only as what they are: without the gate, and with rows of the weights' type."""
+    with pytest.raises(tg.GemmError) as e:
+        tg.GroupMlpPlan(8, 65, 2, 128, 64, weight_type, BT, gated, tg.GEMM_EPI_BIAS_SILU)
+    text = str(e.value)
+    assert "gemm_group_run" in text
+    assert ("gate" in text) == gated and ("e4m3 rows" in text) == (weight_type == tg.GEMM_TYPE_E4M3)

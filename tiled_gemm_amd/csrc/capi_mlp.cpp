@@ -40,11 +40,6 @@ gemm_group_mlp_plan *gemm_group_mlp_plan_create(int groups, int64_t tokens, int 
         capi_fail(GEMM_ERR_INVALID_ARG, "tokens=%lld is negative or topk=%d below 1", (long long)tokens, topk);
         return nullptr;
     }
-    if (tokens > GEMM_GROUP_MLP_MAX_TOKENS || topk > GEMM_GROUP_MLP_MAX_TOPK) {
-        capi_fail(GEMM_ERR_UNSUPPORTED, "tokens=%lld above %d or topk=%d above %d (gemm_group_run has no such limit)",
-                  (long long)tokens, GEMM_GROUP_MLP_MAX_TOKENS, topk, GEMM_GROUP_MLP_MAX_TOPK);
-        return nullptr;
-    }
     if (weight_type != GEMM_TYPE_BF16 && weight_type != GEMM_TYPE_E4M3) {
         if (weight_type == GEMM_TYPE_F32)
             capi_fail(GEMM_ERR_UNSUPPORTED, "the layer's weights are bf16 or e4m3");
@@ -66,6 +61,14 @@ gemm_group_mlp_plan *gemm_group_mlp_plan_create(int groups, int64_t tokens, int 
     }
     if (epilogue < GEMM_EPI_NONE || epilogue > GEMM_EPI_BIAS_GELU) {
         capi_fail(GEMM_ERR_INVALID_ARG, "unknown epilogue %d", epilogue);
+        return nullptr;
+    }
+    if (tokens > GEMM_GROUP_MLP_MAX_TOKENS || topk > GEMM_GROUP_MLP_MAX_TOPK) {
+        capi_fail(GEMM_ERR_UNSUPPORTED,
+                  "tokens=%lld above %d or topk=%d above %d (gemm_group_run's products have no such limit%s%s)",
+                  (long long)tokens, GEMM_GROUP_MLP_MAX_TOKENS, topk, GEMM_GROUP_MLP_MAX_TOPK,
+                  gated ? ", but do not multiply by the gate" : "",
+                  weight_type == GEMM_TYPE_E4M3 ? ", but take e4m3 rows beside e4m3 weights" : "");
         return nullptr;
     }
     if (K < 1 || N < 1) {
