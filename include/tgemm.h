@@ -806,7 +806,9 @@ int gemm_ckpt_unpack(int64_t M, int64_t N, int type, int epilogue, const void *q
 
 /*
  * gemm_act_grad_ckpt -- gemm_act_grad with z read from its checkpoint (q and
- * scales may be NULL without an activation).  d_z may be d_c, and overlaps
+ * scales may be NULL without an activation).  GELU's normal distribution is
+ * within 2^-23 in fp32 and, here and in gemm_ckpt_unpack, within 2^-21 (before
+ * the result's rounding; d_bias sums it as it is) in bf16.  d_z may be d_c, and overlaps
  * neither q nor scales.  The workspace is gemm_act_grad_workspace_bytes.
  */
 int gemm_act_grad_ckpt(int64_t M, int64_t N, int type, int epilogue, const void *d_c, const void *q,

@@ -30,11 +30,12 @@ constexpr int kPackRows = 2, kUnpackRows = 4;
 // A launch has fewer than 2^32 threads.
 constexpr int64_t kCkptBlocks = (int64_t)1 << 23;
 
-template <int ACT>
+// (GELU: normal_cdf's error shows in fp32 only; see there.)
+template <int T, int ACT>
 __device__ inline float ckpt_act(float z)
 {
     float e;
-    return ACT == kActSilu ? epi_silu(z) : ACT == kActGelu ? z * normal_cdf(z, e) : epi_act(z, ACT);
+    return ACT == kActSilu ? epi_silu(z) : ACT == kActGelu && T == kOutBf16 ? z * normal_cdf(z, e) : epi_act(z, ACT);
 }
 
 // The largest of the 4 lanes' values that share a block.
@@ -135,7 +136,7 @@ __global__ __launch_bounds__(kCkptThreads) void ckpt_unpack_kernel(const CkptArg
             ckpt_value8(w[r], e8m0_value(byte[r]), v);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                v[i] = ckpt_act<ACT>(v[i]);
+                v[i] = ckpt_act<T, ACT>(v[i]);
             if (p.row + r < a.M)
                 store8<T>(a.out, (size_t)(p.row + r) * a.N + p.col, v);
         }

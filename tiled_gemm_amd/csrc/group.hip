@@ -353,7 +353,7 @@ __device__ inline float act_slope(float z)
 // The same slopes with fewer instructions, for the checkpoint's fewer bytes.
 // SiLU: the logistic factor takes any z, NaN among them, so only the other factor
 // is kept finite, in one instruction; equal to act_slope bit for bit while
-// |z| <= 100.  GELU: normal_cdf for erff (1013 x 2112 in 16 groups: 10.4 -> 8.0 us).
+// |z| <= 100.  GELU in bf16: normal_cdf for erff (1013 x 2112 in 16 groups: 10.4 -> 8.0 us).
 __device__ inline float silu_slope(float z)
 {
     const float p = __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z * -1.44269504088896340736f));
@@ -367,12 +367,12 @@ __device__ inline float gelu_slope(float z)
     return cdf + __builtin_amdgcn_fmed3f(z, -100.f, 100.f) * (0.39894228040143267794f * e);
 }
 
-template <int ACT, bool CK>
+template <int T, int ACT, bool CK>
 __device__ inline float grad_slope(float z)
 {
     if constexpr (CK && ACT == kActSilu)
         return silu_slope(z);
-    else if constexpr (CK && ACT == kActGelu)
+    else if constexpr (CK && ACT == kActGelu && T == kOutBf16)
         return gelu_slope(z);
     else
         return act_slope<ACT>(z);
@@ -414,7 +414,7 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(const ActGradArgs
                     load8<T>(a.z, at, z);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    d[i] *= grad_slope<ACT, CK>(z[i]);
+                    d[i] *= grad_slope<T, ACT, CK>(z[i]);
             }
             store8<T>(a.d_z, at, d);
 #pragma unroll
