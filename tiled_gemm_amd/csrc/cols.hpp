@@ -26,7 +26,8 @@ __device__ inline void load8(const void *base, size_t at, float (&v)[8])
     }
 }
 
-// Two fp32 -> two bf16 (nearest even) in one instruction, packed low-first.
+// Two fp32 -> two bf16 (nearest even) in one instruction, packed low-first: the bits
+// of pack_bf16x2, which converts them one by one and joins them.
 __device__ inline uint32_t pack_pair(float lo, float hi)
 {
     typedef float f32x2 __attribute__((ext_vector_type(2)));

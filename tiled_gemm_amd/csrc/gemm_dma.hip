@@ -422,6 +422,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_dma_kernel(const Tiled
 
     // (of a split K the first slice's partial tile takes the adapters' share)
     if constexpr (LORA) {
+        static_assert(lora_lds_bytes<DM_BM, lora_planes<OUT>()>() <= DM_LDS, "v fits the stages");
         if (sk.kt0 == 0)
             lora_tail<DM_BM, THREADS, lora_planes<OUT>()>(p.lora, acc, lds, m0, rows_a, wm * WTM, n0 + wn * WTN, p.N);
     }

@@ -477,6 +477,7 @@ __global__ __launch_bounds__(64 * WGM * WGN, 1) void gemm_pipe_kernel(const Tile
         mfma_drain_acc(acc);
     // (of a split K the first slice's partial tile takes the adapters' share)
     if constexpr (LORA) {
+        static_assert(lora_lds_bytes<BP_BM, lora_planes<OUT>()>() <= Cfg::LDS, "v fits the stages");
         if (sk.kt0 == 0)
             lora_tail<BP_BM, 64 * WAVES, lora_planes<OUT>()>(p.lora, acc, lds, m0, rows_a, wm * BP_WTM, n0 + wn * BP_WTN, p.N);
     }

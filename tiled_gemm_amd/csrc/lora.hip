@@ -22,6 +22,7 @@
 //     the block's own workgroup, 16 of them took 260 us (4001 x 4160, rank 64).  As it
 //     is 18 us for 42 MB with them, 14.8 us for 34 MB with one adapter: 2.3 TB/s, a
 //     few steps of K per wave, so mostly latency.
+#include "lora.hpp"
 #include "stream.hpp"
 
 namespace tg {
@@ -107,12 +108,6 @@ __device__ inline void lora_down(const LoraArgs &a, int m0, unsigned long long t
     }
 }
 
-__device__ inline int row_id(const LoraArgs &a, bool there, int row)
-{
-    const int id = there ? a.adapter[row] : -1;
-    return (uint32_t)id < (uint32_t)a.adapters ? id : -1;
-}
-
 }  // namespace
 
 __global__ __launch_bounds__(kStreamThreads, 4) void lora_down_few_kernel(const LoraArgs a)
@@ -121,7 +116,7 @@ __global__ __launch_bounds__(kStreamThreads, 4) void lora_down_few_kernel(const 
     const int m0 = blockIdx.x * 16, l = lane_id();
     const int rb = blockIdx.z / a.parts, part = blockIdx.z - rb * a.parts;
     unsigned long long same = 0;
-    const int e = lora_nth(row_id(a, l < 16 && m0 + l < a.M, m0 + l), ~0ull, blockIdx.y, &same);
+    const int e = lora_nth(lora_id(a, l < 16 && m0 + l < a.M, m0 + l), ~0ull, blockIdx.y, &same);
     if (e < 0)                                       // (most workgroups, where rows share adapters)
         return;
     auto find = [&](unsigned long long *rows) {
@@ -165,7 +160,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
     const int l = lane_id(), rb = blockIdx.y, part = blockIdx.z;
     if ((int)blockIdx.x >= more) {
         const int m0 = ((int)blockIdx.x - more) * 16 * MB;
-        const int id = row_id(a, l < 16 * MB && m0 + l < a.M, m0 + l);
+        const int id = lora_id(a, l < 16 * MB && m0 + l < a.M, m0 + l);
         auto find = [&](unsigned long long *rows) { return lora_nth(id, ~0ull, 0, rows); };
         lora_down<MB, NB>(a, m0, ~0ull, find, rb, part, red);
         return;
@@ -180,7 +175,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
 #pragma unroll
             for (int u = 0; u < 8; ++u) {            // in flight together
                 const int row = (g0 + i + u) * 64 + l;
-                id[u] = row_id(a, row < a.M, row);
+                id[u] = lora_id(a, row < a.M, row);
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
@@ -199,7 +194,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void lora_down_many_kernel(const
                     k = last;
                     continue;
                 }
-                const int id = row_id(a, g * 64 + l < a.M, g * 64 + l);
+                const int id = lora_id(a, g * 64 + l < a.M, g * 64 + l);
                 for (int b = 0; b < 4 / MB; ++b) {
                     const unsigned long long mask = (~0ull >> (64 - 16 * MB)) << (16 * MB * b);
                     unsigned long long left = __ballot(id >= 0) & mask;
