@@ -962,11 +962,14 @@ int ext_from(const gemm_plan *plan, const void *A, const void *B, const void *C,
 }
 
 // Whether adapters go with split K.  Up to K = 8192 the tiles with more steps in
-// flight (plan_ex) take less than slices, partial tiles and their sum: 4 adapters
-// of rank 32, split against not: 310 x 1264 x 2432 51 / 24 us, 200 x 4096 x 4096
-// 48 / 31, 900 x 2048 x 8192 80 / 73, 512 x 8192 x 8192 95 / 100; above it splitting
-// does: 300 x 2048 x 12288 68 / 79, 128 x 2048 x 16384 60 / 89.  Plans without such
-// tiles split as they are: 700 x 8192 x 8192 120 / 176.
+// flight (plan_ex) take less than slices, partial tiles and their sum, or as much:
+// 4 adapters of rank 32, split against not: 310 x 1264 x 2432 51 / 24 us, 200 x 4096 x
+// 4096 48 / 31, 200 x 4096 x 8192 65 / 53, 900 x 2048 x 8192 82 / 73, 512 x 8192 x 8192
+// 107 / 105, 128 x 2048 x 8192 47 / 49.  Where it turns depends on the grid: 128 x 2048
+// 51 / 54 at 9216 and 51 / 59 at 10240, 512 x 8192 118 / 118 and 127 / 132, but 900 x 2048
+// 94 / 81 and 103 / 89, 200 x 4096 71 / 60 and 72 / 65; at 12288 splitting takes less:
+// 300 x 2048 73 / 78, 512 x 8192 142 / 154, 128 x 2048 x 16384 60 / 89.  Plans without
+// such tiles split as they are: 700 x 8192 x 8192 120 / 176.
 bool lora_splits(const gemm_plan *plan)
 {
     return plan->splits > 1 && (plan->split_forced || plan->ex_v == plan->tiled || plan->kbytes > 8192 * 2);

@@ -21,7 +21,10 @@
 //     more (more_of), which read the rows of theirs only.  One after the other in
 //     the block's own workgroup, 16 of them took 260 us (4001 x 4160, rank 64).  As it
 //     is 18 us for 42 MB with them, 14.8 us for 34 MB with one adapter: 2.3 TB/s, a
-//     few steps of K per wave, so mostly latency.
+//     few steps of K per wave, so mostly latency.  Rows in random order, where
+//     every block has all adapters, are what this form is not made for: both
+//     halves for 1000 / 3000 x 4096 x 4160, rank 64, 16 adapters 193 / 507 us, packed
+//     81 / 139; 8192 x 4096 x 4096, rank 16, 64 adapters 1783, packed 255.
 #include "lora.hpp"
 #include "stream.hpp"
 
@@ -248,8 +251,10 @@ hipError_t many_mb(const LoraArgs &a, int blocks, hipStream_t s)
 // per CU, that of 16 or 32 rows two or more).  4001 x 4160 and rank 64 in packed
 // prompts: 22.3 us with the 3 parts that make one round of them, 24.6 with 4;
 // 8000 x 4160 with one adapter 28.3 with 2, 31.0 with 4.  64 rows by 32 ranks leave
-// two workgroups per CU, but the tiles read every part: 8192 x 8192 x 2048 takes 326 us
-// in all with 2 parts, 334 with 4.
+// two workgroups per CU, but counted as one they take as long or less, as the tiles
+// read every part: 8192 x 8192 x 2048 one adapter 308 us in all with 2 parts, 315 with 4;
+// 4096 x 4096 x 4096 packed 134 / 138, 6000 x 2048 x 2048 73 / 75, 8192 x 4096 x 4096 250 / 249,
+// 3000 x 8192 x 8192 382 / 382.
 int lora_parts(int64_t M, int64_t K, int rank_pad, int adapters)
 {
     const int64_t most = K * 2 / kStepBytes / kStreamWaves;
